@@ -1,0 +1,449 @@
+"""The key/value cache in 4 bits: the cases its operators are measured at, their plain forms and their exact values.
+
+Three operators of one decode step's or prompt's attention block share one paged cache:
+
+* append: k and v rows of new tokens are quantised into the pages (and read back as the values the 4 bits stand for);
+* attention: query rows over the pages, one token per sequence or many, optionally with the log-sum-exp of each row and
+  with the attention weight that each cached token received added to an accumulator;
+* evict: the tokens that accumulated the least attention weight leave the cache, the rest move together.
+
+The format.  A group is g consecutive channels of one token and kv head.  Its values, clamped to +-32768, are held as
+lo + s u with lo = fp16(min), s = fp16(fp32((max - min) / 15)) (difference and quotient in binary32) and
+u = #{j in 0..14 : x >= lo + (j + 1/2) s}, the nearest code with ties upward (0 where s = 0).
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+DT = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}
+GPU = "cuda:0"
+
+
+# ---------------------------------------------------------------- cases ----
+def listed():
+    att = dict(kind="attention", Hq=32, Hkv=8, D=128, g=64, P=64, dtype="fp16", causal=True, window=0, lse=False,
+               weights=False, wide=1)
+    app = dict(kind="append", Hkv=8, D=128, g=64, P=64, dtype="fp16")
+    ev = dict(kind="evict", Hkv=8, D=128, g=64, P=64, dtype="fp16")
+    return [
+        # one user, a short chat: a decode step where only latency counts
+        dict(att, name="attend_one_short", B=1, T=1, L=217, mix=0),
+        # one user deep in a long document: the cache is the whole cost of the step
+        dict(att, name="attend_one_long", B=1, T=1, L=131001, mix=0, lse=True),
+        # a serving batch of ragged lengths, page table sized for longer ones, an idle slot among them
+        dict(att, name="attend_batch", B=32, T=1, L=4099, mix=3, Hq=40, Hkv=10, g=128, dtype="bf16", wide=2),
+        # decode with the weight of every cached token accumulated for a later eviction
+        dict(att, name="attend_batch_weights", B=8, T=1, L=16000, mix=5, weights=True),
+        # a few drafted tokens verified at once under a sliding window, small heads, finer groups
+        dict(att, name="attend_draft_window", B=16, T=6, L=8191, mix=7, Hq=16, Hkv=4, D=64, g=32, P=32, window=1024),
+        # a whole prompt against itself
+        dict(att, name="attend_prompt", B=1, T=8192, L=8192, mix=0, dtype="bf16"),
+        # ragged chunks of prompts over what is cached, with the weights an eviction after the prompt needs
+        dict(att, name="attend_chunk_weights", B=2, T=1000, L=12001, mix=11, P=128, lse=True, weights=True),
+        # the decode step's new rows, every sequence one token
+        dict(app, name="append_step", B=64, T=1, L=5000, mix=13),
+        # a prompt's rows
+        dict(app, name="append_prompt", B=1, T=8192, L=8192, mix=0, dtype="bf16"),
+        # ragged rows straight from fp32 products, odd head size
+        dict(app, name="append_ragged", B=7, T=333, L=2100, mix=17, Hkv=5, D=96, g=32, P=32, dtype="fp32"),
+        # a batch brought back to its budget
+        dict(ev, name="evict_batch", B=4, L=4096, mix=19, keep=1024, sinks=4, recent=256),
+        # one long context cut to an eighth
+        dict(ev, name="evict_long", B=1, L=65536, mix=0, keep=8192, sinks=4, recent=1001, P=128, g=128),
+    ]
+
+
+def _log(rng, a, b):
+    return int(round(math.exp(rng.uniform(math.log(a), math.log(b)))))
+
+
+def draw(rng):
+    kind = rng.choice(["attention", "attention", "attention", "append", "evict"])
+    D = rng.choice([64, 96, 128, 128, 128, 256])
+    g = rng.choice([x for x in (32, 64, 128) if D % x == 0])
+    P = rng.choice([32, 64, 128, 256])
+    Hkv = rng.choice([1, 2, 3, 4, 8, 8, 10])
+    case = dict(kind=kind, Hkv=Hkv, D=D, g=g, P=P, mix=rng.randrange(1, 1000))
+    room = 131001 * 8 * 128                       # values of K in the largest listed cache
+    if kind == "attention":
+        case.update(Hq=Hkv * rng.choice([1, 2, 3, 4, 5, 8, 16]), dtype=rng.choice(["fp16", "bf16"]),
+                    causal=rng.random() < 0.85, window=0, lse=rng.random() < 0.5, weights=rng.random() < 0.4,
+                    wide=rng.choice([1, 1, 3]))
+        case["B"] = _log(rng, 1, 48)
+        case["T"] = rng.choice([1, 1, 1, rng.randrange(2, 9), _log(rng, 9, 2048)])
+        if case["T"] > 8:
+            case["B"] = min(case["B"], 3)
+        case["L"] = min(_log(rng, 1, 100000), room // (case["B"] * Hkv * D))
+        case["L"] = max(1, min(case["L"], 8192 * 8192 * 32 // (2 * case["T"] * case["Hq"] * case["B"])))
+        if case["causal"] and rng.random() < 0.3:
+            case["window"] = _log(rng, 1, 4096)
+    elif kind == "append":
+        case.update(dtype=rng.choice(["fp16", "bf16", "fp32"]), B=_log(rng, 1, 64))
+        case["T"] = rng.choice([1, _log(rng, 1, 8192)])
+        case["T"] = max(1, min(case["T"], 8192 * 8 * 128 // (case["B"] * Hkv * D)))
+        case["L"] = case["T"] + _log(rng, 1, 4000) - 1
+    else:
+        case.update(dtype=rng.choice(["fp16", "bf16"]), B=_log(rng, 1, 8))
+        case["L"] = min(_log(rng, 40, 65536), 65536 * 8 * 128 // (case["B"] * Hkv * D))
+        case["keep"] = max(1, min(8192, int(case["L"] * rng.uniform(0.05, 0.9))))
+        case["sinks"] = rng.choice([0, min(4, case["keep"] // 2)])
+        case["recent"] = rng.randrange(0, case["keep"] - case["sinks"] + 1)
+    return case
+
+
+def _lengths(case):
+    """Tokens cached (this step's among them) and new ones, per sequence: from the case alone.  mix 0: all full."""
+    B, L, T = case["B"], case["L"], case.get("T", 1)
+    if not case["mix"]:
+        return [L] * B, [min(T, L)] * B
+    r = random.Random(case["mix"])
+    lens = [L] + [_log(r, max(1, L / 12), L) for _ in range(B - 1)]
+    new = [min(T, n) if i == 0 else min(n, r.randint((T + 1) // 2, T)) for i, n in enumerate(lens)]
+    if B >= 4:                                    # an idle slot, and a sequence at its first token
+        lens[1], new[1], lens[2], new[2] = 0, 0, 1, 1
+    return lens, new
+
+
+# --------------------------------------------------------------- inputs ----
+def _inputs(case, seed):
+    gen = torch.Generator(device=GPU)
+    gen.manual_seed(seed * 7919 + 11)
+    B, L, Hkv, D, P = case["B"], case["L"], case["Hkv"], case["D"], case["P"]
+    T, dt = case.get("T", 1), DT[case["dtype"]]
+    lens, new = _lengths(case)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device=GPU)
+    rows = T if case["kind"] == "append" else L
+    Hq = case.get("Hq", 0)
+    # keys: per-channel offsets and a few wide channels, as rotary keys show them; a first token that draws weight
+    spread = 0.5 + rnd(Hkv, D).abs()
+    spread[:, :: max(1, D // 5)] *= 3.0
+    lean = rnd(Hkv, D)
+    k = rnd(B, rows, Hkv, D).mul_(spread).add_(lean * 0.7)
+    k[:, 0] += 1.5 * lean
+    v = rnd(B, rows, Hkv, D).mul_(0.2 + 0.6 * torch.rand(B, rows, Hkv, 1, generator=gen, device=GPU))
+    x = dict(lens=lens, new=new)
+    if case["kind"] == "append":                  # slices of one row of q, k and v together
+        both = torch.empty(B, T, 2, Hkv, D, dtype=dt, device=GPU)
+        both[:, :, 0], both[:, :, 1] = k, v
+        x["k"], x["v"] = both[:, :, 0], both[:, :, 1]
+    else:
+        x["k"], x["v"] = k.to(dt), v.to(dt)
+    if case["kind"] == "attention":
+        q = rnd(B, T, Hkv, Hq // Hkv, D).mul_(0.6).add_(0.15 * lean[:, None])
+        fused = torch.empty(B, T, (Hq + 2 * Hkv) * D, dtype=dt, device=GPU)
+        fused[..., : Hq * D] = q.reshape(B, T, Hq * D)
+        x["q"] = fused[..., : Hq * D].view(B, T, Hq, D)
+    # pages handed out in no order, table entries past a sequence's last page unused
+    width = -(-L // P)
+    need = [-(-n // P) for n in lens]
+    total = sum(need)
+    perm = torch.randperm(total + 3, generator=gen, device=GPU)[:total].to(torch.int32)
+    table = torch.full((B, width * case.get("wide", 1)), -1, dtype=torch.int32, device=GPU)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at: at + n]
+        at += n
+    x.update(table=table, pages=total + 3)
+    if case["kind"] == "attention" and case["weights"]:
+        x["weights"] = torch.rand(B, Hkv, L, generator=gen, device=GPU) * 3.0
+    if case["kind"] == "evict":                   # what many steps accumulate: a few heavy tokens, many with nothing
+        w = torch.rand(B, Hkv, L, generator=gen, device=GPU)
+        w = torch.where(w < 0.3, torch.zeros_like(w), (-torch.log(w.clamp(min=1e-6))) ** 3)
+        for b, n in enumerate(lens):
+            w[b, :, n:] = 0
+        x["weights"] = w
+        per = -(-case["keep"] // P)
+        x["out_table"] = torch.arange(B * per, dtype=torch.int32, device=GPU).view(B, per) + x["pages"]
+        x["pages"] += B * per
+    return x
+
+
+def prepare(case, seed):
+    x = _inputs(case, seed)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=GPU)
+    st = dict(case=case, lens=x["lens"], new=x["new"], table=x["table"], lengths=i32(x["lens"]), new_lens=i32(x["new"]),
+              start=i32([n - m for n, m in zip(x["lens"], x["new"])]))
+    for key in ("q", "weights", "out_table"):
+        if key in x:
+            st[key] = x[key]
+    Hkv, D, g, P = case["Hkv"], case["D"], case["g"], case["P"]
+    if case["kind"] == "append":
+        st["k"], st["v"] = x["k"], x["v"]
+    if own:
+        import precision_weight_only_amd as pwo
+        st["cache"] = pwo.KVCache(x["pages"], Hkv, D, group=g, page_tokens=P, device=GPU)
+        if case["kind"] != "append":
+            st["cache"].append(x["k"], x["v"], x["table"], st["lengths"], new_lens=st["lengths"])
+    else:
+        n = x["pages"]
+        st["codes"] = torch.zeros(2, n, P, Hkv, D // 2, dtype=torch.uint8, device=GPU)
+        st["pairs"] = torch.zeros(2, n, P, Hkv, D // g, 2, dtype=torch.float16, device=GPU)
+        if case["kind"] != "append":
+            for b, m in enumerate(x["lens"]):
+                for at in range(0, m, 16384):
+                    end = min(m, at + 16384)
+                    _plain_append(st, b, at, x["k"][b, at:end], x["v"][b, at:end])
+    return st
+
+
+# ---------------------------------------------------------- plain forms ----
+def _plain_quantise(x, g):
+    """x [n, H, D] -> (codes uint8 [n, H, D], pairs fp16 [n, H, D/g, 2])."""
+    n, H, D = x.shape
+    x = x.float().clamp(-32768.0, 32768.0).view(n, H, D // g, g)
+    mn, mx = x.amin(-1), x.amax(-1)
+    lo = mn.half()
+    s = ((mx - mn).double() / 15.0).float().half()
+    lo64, s64, x64 = lo.double().unsqueeze(-1), s.double().unsqueeze(-1), x.double()
+    u = torch.floor((x64 - lo64) / torch.where(s64 > 0, s64, torch.ones_like(s64)) + 0.5).clamp(0, 15)
+    u = torch.where((u < 15) & (x64 >= lo64 + (u + 0.5) * s64), u + 1, u)   # values next to a border
+    u = torch.where((u > 0) & (x64 < lo64 + (u - 0.5) * s64), u - 1, u)
+    u = torch.where(s64 > 0, u, torch.zeros_like(u))
+    return u.to(torch.uint8).view(n, H, D), torch.stack([lo, s], -1)
+
+
+def _plain_slots(st, b, start, end):
+    P = st["case"]["P"]
+    t = torch.arange(start, end, device=GPU)
+    return st["table"][b].long()[t // P] * P + t % P
+
+
+def _plain_append(st, b, start, k, v):
+    at = _plain_slots(st, b, start, start + k.shape[0])
+    for i, x in enumerate((k, v)):
+        u, pairs = _plain_quantise(x, st["case"]["g"])
+        st["codes"][i].flatten(0, 1)[at] = u[..., 0::2] | (u[..., 1::2] << 4)
+        st["pairs"][i].flatten(0, 1)[at] = pairs
+
+
+def _plain_values(codes, pairs):
+    """fp32 values lo + s u of packed codes [n, H, D/2] and pairs [n, H, D/g, 2]."""
+    n, H, half = codes.shape
+    u = torch.stack([codes & 15, codes >> 4], -1).view(n, H, pairs.shape[2], -1).float()
+    return (pairs[..., 0:1].float() + pairs[..., 1:2].float() * u).view(n, H, 2 * half)
+
+
+def _plain_read(st, i, at):
+    return _plain_values(st["codes"][i].flatten(0, 1)[at], st["pairs"][i].flatten(0, 1)[at])
+
+
+def _plain_attention(st):
+    c, q = st["case"], st["q"]
+    B, T, Hq, D = q.shape
+    Hkv, gq, dev = c["Hkv"], q.shape[2] // c["Hkv"], q.device
+    out = torch.zeros(B, T, Hq, D, dtype=q.dtype, device=dev)
+    lse = torch.full((B, T, Hq), -math.inf, dtype=torch.float32, device=dev)
+    weights = st["weights"].clone() if c["weights"] else None
+    for b in range(B):
+        n, t = st["lens"][b], st["new"][b]
+        if n == 0 or t == 0:
+            continue
+        first = max(0, n - t - c["window"] + 1) if c["window"] else 0
+        at = _plain_slots(st, b, first, n)
+        k, v = _plain_read(st, 0, at), _plain_read(st, 1, at)
+        p = torch.arange(n - t, n, device=dev)[:, None]
+        slot = torch.arange(first, n, device=dev)[None]
+        see = torch.ones(t, n - first, dtype=torch.bool, device=dev)
+        if c["causal"]:
+            see &= slot <= p
+        if c["window"]:
+            see &= slot > p - c["window"]
+        for h in range(Hkv):
+            qh = q[b, :t, h * gq:(h + 1) * gq].float().permute(1, 0, 2)
+            z = torch.matmul(qh, k[:, h].t()) * (1.0 / math.sqrt(D))
+            z = z.masked_fill(~see, -math.inf)
+            m = z.amax(-1, keepdim=True).clamp(min=-3e38)
+            e = torch.exp(z - m)
+            l = e.sum(-1, keepdim=True)
+            w = e / l.clamp(min=1e-38)
+            out[b, :t, h * gq:(h + 1) * gq] = torch.matmul(w, v[:, h]).permute(1, 0, 2).to(q.dtype)
+            lse[b, :t, h * gq:(h + 1) * gq] = (m + torch.log(l)).squeeze(-1).t()
+            if weights is not None:
+                weights[b, h, first:n] += w.sum((0, 1))
+    return _attention_outputs(c, out, lse, weights)
+
+
+def _attention_outputs(c, out, lse, weights):
+    res = {"out": out}
+    if c["lse"]:
+        res["lse"] = lse
+    if c["weights"]:
+        res["weights"] = weights
+    return res
+
+
+def _plain_evict(st):
+    c, w = st["case"], st["weights"]
+    B, Hkv, L = w.shape
+    keep, D, dev = c["keep"], c["D"], w.device
+    kept = torch.full((B, Hkv, keep), -1, dtype=torch.int32, device=dev)
+    wout = torch.zeros_like(w)
+    k = torch.zeros(B, keep, Hkv, D, dtype=torch.float16, device=dev)
+    v = torch.zeros_like(k)
+    head = torch.arange(Hkv, device=dev)
+    for b in range(B):
+        n = st["lens"][b]
+        m = min(n, keep)
+        if m == 0:
+            continue
+        rank = w[b, :, :n].clone()
+        if n > keep:
+            rank[:, : c["sinks"]] = math.inf
+            rank[:, n - c["recent"]:] = math.inf
+        order = torch.sort(rank, dim=-1, descending=True, stable=True).indices[:, :m]
+        pick = torch.sort(order, dim=-1).values
+        kept[b, :, :m] = pick.int()
+        wout[b, :, :m] = torch.gather(w[b], 1, pick)
+        src = _plain_slots(st, b, 0, n)[pick.t()]                      # [m, Hkv] page slots
+        P = c["P"]
+        t = torch.arange(m, device=dev)
+        dst = st["out_table"][b].long()[t // P] * P + t % P
+        for i, o in ((0, k), (1, v)):
+            codes, pairs = st["codes"][i].flatten(0, 1), st["pairs"][i].flatten(0, 1)
+            codes[dst], pairs[dst] = codes[src, head], pairs[src, head]
+            o[b, :m] = _plain_values(codes[dst], pairs[dst]).half()
+    return {"kept": kept, "lengths": st["lengths"].clamp(max=keep), "weights": wout, "k": k, "v": v}
+
+
+def _plain_append_and_read(st):
+    c = st["case"]
+    k = torch.zeros(c["B"], c["T"], c["Hkv"], c["D"], dtype=torch.float32, device=GPU)
+    v = torch.zeros_like(k)
+    for b in range(c["B"]):
+        t, start = st["new"][b], st["lens"][b] - st["new"][b]
+        if t:
+            _plain_append(st, b, start, st["k"][b, :t], st["v"][b, :t])
+            at = _plain_slots(st, b, start, start + t)
+            k[b, :t], v[b, :t] = _plain_read(st, 0, at), _plain_read(st, 1, at)
+    return {"k": k, "v": v}
+
+
+# ------------------------------------------------------------------ run ----
+def run(st):
+    c = st["case"]
+    if not own:
+        return {"attention": _plain_attention, "append": _plain_append_and_read, "evict": _plain_evict}[c["kind"]](st)
+    cache = st["cache"]
+    ragged = st["new_lens"] if c["mix"] else None
+    if c["kind"] == "append":
+        cache.append(st["k"], st["v"], st["table"], st["lengths"], new_lens=ragged)
+        k, v = cache.read(st["table"], st["lengths"], tokens=c["T"], start=st["start"])
+        return {"k": k, "v": v}
+    if c["kind"] == "evict":
+        wout = torch.empty_like(st["weights"])
+        kept, lengths = cache.evict(st["table"], st["lengths"], st["weights"], c["keep"], sinks=c["sinks"],
+                                    recent=c["recent"], out_table=st["out_table"], weights_out=wout)
+        k, v = cache.read(st["out_table"], lengths, tokens=c["keep"], dtype=torch.float16)
+        return {"kept": kept, "lengths": lengths, "weights": wout, "k": k, "v": v}
+    lse = torch.empty(st["q"].shape[:3], dtype=torch.float32, device=GPU) if c["lse"] else None
+    if c["lse"] and c["mix"]:
+        lse.fill_(-math.inf)                      # rows past a sequence's new tokens are not written
+    weights = st["weights"].clone() if c["weights"] else None
+    out = cache.attention(st["q"], st["table"], st["lengths"], q_lens=ragged, causal=c["causal"], window=c["window"],
+                          max_len=c["L"], lse=lse, weights=weights)
+    return _attention_outputs(c, out, lse, weights)
+
+
+# ----------------------------------------------------------------- work ----
+def work(case):
+    lens, new = _lengths(case)
+    Hkv, D, g = case["Hkv"], case["D"], case["g"]
+    row = Hkv * (D + 8 * (D // g))                # K and V of one token in 4 bits, with their pairs
+    size = {"fp16": 2, "bf16": 2, "fp32": 4}[case["dtype"]]
+    if case["kind"] == "append":
+        n = sum(new)
+        return {"bytes": n * (2 * Hkv * D * (size + 4) + row), "flops": n * 2 * Hkv * D * 6}
+    if case["kind"] == "evict":
+        m = sum(min(n, case["keep"]) for n in lens)
+        return {"bytes": 4 * Hkv * sum(lens) + m * (8 * Hkv + 2 * row + 4 * Hkv * D), "flops": Hkv * sum(lens)}
+    win, seen, pairs = case["window"], 0, 0
+    for n, t in zip(lens, new):
+        if t == 0:
+            continue
+        seen += min(n, win + t - 1) if win else n
+        for p in range(n - t, n):
+            m = p + 1 if case["causal"] else n
+            pairs += min(m, win) if win else m
+    q = sum(new) * case["Hq"]
+    return {"bytes": seen * row + 2 * q * D * size + (4 * q if case["lse"] else 0)
+            + (8 * seen * Hkv if case["weights"] else 0), "flops": 4 * D * case["Hq"] * pairs}
+
+
+# ---------------------------------------------------------------- exact ----
+def _exact_values(x, g):
+    """float64 values that 4 bits hold for x [n, D] (or any leading sizes): every border compared, exactly."""
+    shape = x.shape
+    x = x.double().clamp(-32768.0, 32768.0).reshape(-1, g)
+    mn, mx = x.min(1, keepdim=True).values, x.max(1, keepdim=True).values
+    lo = mn.float().half().double()
+    s = ((mx.float() - mn.float()).double() / 15).float().half().double()
+    u = torch.zeros_like(x)
+    for j in range(15):
+        u += x >= lo + (j + 0.5) * s
+    return (lo + s * u * (s > 0)).reshape(shape)
+
+
+def exact(case, seed):
+    x = _inputs(case, seed)
+    lens, new, g, D, Hkv = x["lens"], x["new"], case["g"], case["D"], case["Hkv"]
+    if case["kind"] == "append":
+        res = {}
+        for key in ("k", "v"):
+            o = torch.zeros(x[key].shape, dtype=torch.float64, device=GPU)
+            for b, t in enumerate(new):
+                if t:
+                    o[b, :t] = _exact_values(x[key][b, :t], g)
+            res[key] = o
+        return res
+    if case["kind"] == "evict":
+        keep, w = case["keep"], x["weights"]
+        kept = torch.full((case["B"], Hkv, keep), -1, dtype=torch.int32, device=GPU)
+        wout = torch.zeros(w.shape, dtype=torch.float64, device=GPU)
+        k = torch.zeros(case["B"], keep, Hkv, D, dtype=torch.float64, device=GPU)
+        v = torch.zeros_like(k)
+        host = w.cpu().tolist()
+        for b, n in enumerate(lens):
+            for h in range(Hkv):
+                if n <= keep:
+                    pick = list(range(n))
+                else:
+                    middle = range(case["sinks"], n - case["recent"])
+                    heavy = sorted(middle, key=lambda t: (-host[b][h][t], t))[: keep - case["sinks"] - case["recent"]]
+                    pick = sorted(list(range(case["sinks"])) + heavy + list(range(n - case["recent"], n)))
+                if not pick:
+                    continue
+                kept[b, h, : len(pick)] = torch.tensor(pick, dtype=torch.int32, device=GPU)
+                at = torch.tensor(pick, device=GPU)
+                wout[b, h, : len(pick)] = w[b, h, at].double()
+                k[b, : len(pick), h] = _exact_values(x["k"][b, at, h], g)
+                v[b, : len(pick), h] = _exact_values(x["v"][b, at, h], g)
+        lengths = torch.tensor([min(n, keep) for n in lens], dtype=torch.int32, device=GPU)
+        return {"kept": kept, "lengths": lengths, "weights": wout, "k": k, "v": v}
+    B, T, Hq = case["B"], case["T"], case["Hq"]
+    gq = Hq // Hkv
+    out = torch.zeros(B, T, Hq, D, dtype=torch.float64, device=GPU)
+    lse = torch.full((B, T, Hq), -math.inf, dtype=torch.float64, device=GPU)
+    weights = x["weights"].double() if case["weights"] else None
+    for b, (n, t) in enumerate(zip(lens, new)):
+        for h in range(Hkv if n and t else 0):
+            k, v = _exact_values(x["k"][b, :n, h], g), _exact_values(x["v"][b, :n, h], g)
+            step = max(1, (1 << 27) // (n * gq))
+            for i in range(0, t, step):
+                r = torch.arange(i, min(t, i + step), device=GPU)
+                z = x["q"][b, r, h * gq:(h + 1) * gq].double().reshape(-1, D) @ k.t() / math.sqrt(D)
+                pos = (n - t + r).repeat_interleave(gq)[:, None]
+                slot = torch.arange(n, device=GPU)[None]
+                hide = (slot > pos) if case["causal"] else torch.zeros_like(slot > pos)
+                if case["window"]:
+                    hide = hide | (slot <= pos - case["window"])
+                z[hide] = -math.inf
+                total = torch.logsumexp(z, 1)
+                prob = torch.exp(z - total[:, None])
+                out[b, r, h * gq:(h + 1) * gq] = (prob @ v).view(-1, gq, D)
+                lse[b, r, h * gq:(h + 1) * gq] = total.view(-1, gq)
+                if weights is not None:
+                    weights[b, h, :n] += prob.sum(0)
+    return _attention_outputs(case, out, lse, weights)

@@ -335,7 +335,8 @@ def run(st):
     if c["kind"] == "evict":
         wout = torch.empty_like(st["weights"])
         kept, lengths = cache.evict(st["table"], st["lengths"], st["weights"], c["keep"], sinks=c["sinks"],
-                                    recent=c["recent"], out_table=st["out_table"], weights_out=wout)
+                                    recent=c["recent"], max_len=c["L"], out_table=st["out_table"],
+                                    weights_out=wout)
         k, v = cache.read(st["out_table"], lengths, tokens=c["keep"], dtype=torch.float16)
         return {"kept": kept, "lengths": lengths, "weights": wout, "k": k, "v": v}
     lse = torch.empty(st["q"].shape[:3], dtype=torch.float32, device=GPU) if c["lse"] else None

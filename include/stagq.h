@@ -301,6 +301,151 @@ int stagq_unpack_host(const void* image, size_t image_bytes, stagq_info* shape, 
                       uint8_t* planes, uint16_t* lo, uint16_t* s, int32_t* row_ptr, int32_t* col,
                       uint16_t* val);
 
+/* ------------------------------------------------------------------------
+ * The key/value cache in 4 bits: what a decode step's k and v rows go into,
+ * and the attention that reads it.
+ *
+ * A group is `group` consecutive channels of one token and kv head.  Its
+ * values x (clamped to +-32768; NaN is held as 0) are held as lo + s u with
+ * lo = fp16(min x), s = fp16((max x - min x) / 15) (difference and quotient in
+ * binary32, each rounded to nearest even) and the code
+ * u = #{ j in 0..14 : x >= lo + (j + 1/2) s }, the nearest one with ties
+ * upward; u = 0 where s = 0.
+ *
+ * Tokens live in pages of page_tokens slots; slot t of sequence b is slot
+ * t mod page_tokens of page table[b][t / page_tokens].  A table entry outside
+ * [0, pages) stands for no page: nothing is written there, attention treats
+ * its slots as masked, reads give 0.  Two sequences may share pages that only
+ * attention and reads touch; a call that writes must not write one slot twice.
+ *
+ * Every call checks its arguments on the host, is asynchronous on hip_stream,
+ * allocates nothing and can be captured.  Results do not depend on timing
+ * (fixed orders of summation, no floating-point atomics).
+ */
+
+typedef struct {
+  int32_t pages, page_tokens; /* page_tokens 32, 64, 128 or 256 */
+  int32_t kv_heads;           /* 1..1024 */
+  int32_t head_dim;           /* 64, 96, 128 or 256 */
+  int32_t group;              /* 32, 64 or 128, dividing head_dim */
+  int32_t spare;
+  void* buf;                  /* device, 256-byte aligned, caller-owned */
+  uint64_t bytes;             /* >= stagq_kv_bytes */
+} stagq_kv_cache;
+
+/* Sequences: page table and the tokens each holds, in device memory.  A length
+ * counts the tokens of the call too (append: after it). */
+typedef struct {
+  int32_t batch;
+  int32_t table_width;        /* entries of a row of the table */
+  int64_t table_stride;       /* int32 elements from one row to the next */
+  const int32_t* table;       /* 4-byte aligned */
+  const int32_t* lengths;     /* [batch] */
+} stagq_kv_seqs;
+
+#define STAGQ_F16  0
+#define STAGQ_BF16 1
+#define STAGQ_F32  2
+
+/* A tensor [batch, tokens, heads, head_dim] in device memory: channels
+ * adjacent, the other strides in elements, each a multiple of 8; data 16-byte
+ * aligned. */
+typedef struct {
+  void* data;
+  int32_t dtype;              /* STAGQ_F16, STAGQ_BF16 or STAGQ_F32 */
+  int32_t tokens, heads, spare;
+  int64_t stride_seq, stride_token, stride_head;
+} stagq_kv_tensor;
+
+/* Bytes of the buffer of a cache of this shape (0 if unsupported; buf and
+ * bytes are not looked at). */
+size_t stagq_kv_bytes(const stagq_kv_cache* c);
+
+/*
+ * Quantise new tokens into the cache: row i < n_b of k and v (fp16, bf16 or
+ * fp32, both the same) becomes slot lengths[b] - n_b + i, n_b = new_lens[b]
+ * (clamped to 0..tokens), or tokens for all with new_lens NULL.  Rows from n_b
+ * on are not read; slots before 0 or past the table are dropped.
+ */
+int stagq_kv_append(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_tensor* k,
+                    const stagq_kv_tensor* v, const int32_t* new_lens, void* hip_stream);
+
+/*
+ * The values the cache holds, lo + s u rounded once to the tensors' type: row i
+ * of k and v receives slot start[b] + i (start NULL: slot i) where that is
+ * below lengths[b]; other rows are left as they were.
+ */
+int stagq_kv_read(const stagq_kv_cache* c, const stagq_kv_seqs* q, const int32_t* start,
+                  const stagq_kv_tensor* k, const stagq_kv_tensor* v, void* hip_stream);
+
+/*
+ * Attention of query rows over the cache.  Row i < q_lens[b] (clamped to
+ * 0..q.tokens; NULL: all) stands at position p = lengths[b] - q_lens[b] + i and
+ * sees slot t if t < lengths[b], t <= p where causal, and t > p - window where
+ * window > 0 (which needs causal).  q head h reads kv head
+ * h / (q.heads / kv_heads).  With P = softmax(scale q . k) over what it sees,
+ * out = sum P v; a row that sees nothing gets 0.
+ *   lse      NULL or fp32 [batch, q.tokens, q.heads]: ln sum exp(scale q . k)
+ *            (-inf where nothing is seen)
+ *   weights  NULL or fp32 [batch, kv_heads, >= max_len] with these strides (in
+ *            elements): slot t of kv head h gains the sum of P[t] over the
+ *            sequence's rows and the q heads of h
+ *   max_len  bound of the lengths that sizes the launch (0: the table's width);
+ *            a longer sequence is cut to it
+ * Rows from q_lens[b] on are neither read nor written in q, out and lse.  q and
+ * out are fp16 or bf16, both the same.
+ */
+typedef struct {
+  stagq_kv_tensor q, out;
+  const int32_t* q_lens;
+  float* lse;
+  float* weights;
+  int64_t weights_stride_seq, weights_stride_head;
+  float scale;
+  int32_t causal, window, max_len;
+} stagq_kv_attn;
+
+/* Bytes of device workspace (256-byte aligned) the call needs; it holds nothing
+ * between calls, and calls that may run at the same time need one each.  0 also
+ * for arguments that the call refuses. */
+size_t stagq_kv_attention_workspace(const stagq_kv_cache* c, const stagq_kv_seqs* q,
+                                    const stagq_kv_attn* a);
+int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_attn* a,
+                       void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * Eviction by accumulated attention weight, for every sequence and kv head: of
+ * n = lengths[b] tokens (cut to max_len; 0: the table's width) all stay where
+ * n <= keep; else the first `sinks`, the last `recent`, and of the others the
+ * heaviest (ties: the lowest slot; NaN counts as heaviest), keep in all.  The
+ * tokens that stay move together in their order.
+ *   weights      fp32 [batch, kv_heads, >= max_len]
+ *   weights_out  receives the weights of the tokens that stay, then 0 up to
+ *                max_len; may be weights itself
+ *   kept         int32 [batch, kv_heads, keep]: the slots that stay, ascending,
+ *                then -1
+ *   out_lengths  int32 [batch]: min(n, keep); may be the sequences' lengths
+ *   out_table    pages the tokens move to (none of them among the pages read),
+ *                or NULL: they move within their own pages
+ * 0 <= sinks, recent; sinks + recent <= keep; keep >= 1.
+ */
+typedef struct {
+  const float* weights;
+  float* weights_out;
+  int64_t weights_stride_seq, weights_stride_head, out_stride_seq, out_stride_head;
+  int32_t* kept;
+  int32_t* out_lengths;
+  const int32_t* out_table;
+  int64_t out_table_stride;
+  int32_t out_table_width;
+  int32_t keep, sinks, recent, max_len, spare;
+} stagq_kv_evict_args;
+
+size_t stagq_kv_evict_workspace(const stagq_kv_cache* c, const stagq_kv_seqs* q,
+                                const stagq_kv_evict_args* e);
+int stagq_kv_evict(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_evict_args* e,
+                   void* workspace, size_t workspace_bytes, void* hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

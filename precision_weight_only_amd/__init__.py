@@ -7,6 +7,10 @@ marshal arguments; packing, decoding and the GEMV run in the native library.
     fields = pwo.encode(w_fp16, group=128, nbits=4, budget=K)      # host encoder
     m = pwo.StagQMatrix.pack(fields, device="cuda:0")               # plane-major image in HBM
     y = m.gemv(x_fp16_cuda, bits=3)                                 # precision chosen per call
+
+    cache = pwo.KVCache(pages=512, kv_heads=8, head_dim=128)        # keys and values in 4 bits
+    cache.append(k, v, table, lengths)                              # this step's rows
+    out = cache.attention(q, table, lengths)                        # over everything cached
 """
 from __future__ import annotations
 
@@ -17,13 +21,14 @@ import numpy as np
 
 from . import _lib as _lib_mod
 from ._lib import EXPORTED, Info, StagQError, check, fields_struct, lib  # noqa: F401
+from .kv_cache import KVCache  # noqa: F401
 
 
 def load() -> None:
     """Load libstagq.so now (raises ImportError if it has not been built)."""
     lib()
 
-__all__ = ["StagQMatrix", "encode", "pack_host", "unpack_host", "packed_bytes", "plan_gemv",
+__all__ = ["StagQMatrix", "KVCache", "encode", "pack_host", "unpack_host", "packed_bytes", "plan_gemv",
            "StagQError"]
 
 

@@ -12,12 +12,14 @@ import shutil
 import subprocess
 import sys
 import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libstagq.so")
 ARCH = "gfx950"
+DEVICE_SOURCES = ("stagq_device.hip", "stagq_kv_rows.hip", "stagq_kv_attention.hip", "stagq_kv_evict.hip")
 
 
 def hipcc() -> str:
@@ -45,17 +47,20 @@ def build_library(verbose: bool = False, extra_flags=()) -> str:
     tmpdir = tempfile.mkdtemp(prefix="stagq_build_")
     try:
         host_o = os.path.join(tmpdir, "stagq_host.o")
-        dev_o = os.path.join(tmpdir, "stagq_device.o")
         _run(["g++", "-O3", "-std=c++17", "-fPIC", "-Wall", "-pthread", *inc,
               "-c", os.path.join(CSRC, "stagq_host.cpp"), "-o", host_o], verbose)
-        _run([hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
-              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-Wall",
-              *inc, *extra_flags, "-c", os.path.join(CSRC, "stagq_device.hip"), "-o", dev_o], verbose)
+        dev_o = [os.path.join(tmpdir, os.path.splitext(src)[0] + ".o") for src in DEVICE_SOURCES]
+        cmds = [[hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
+                 "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-Wall",
+                 *inc, *extra_flags, "-c", os.path.join(CSRC, src), "-o", o]
+                for src, o in zip(DEVICE_SOURCES, dev_o)]
+        with ThreadPoolExecutor(max_workers=4) as pool:
+            list(pool.map(lambda cmd: _run(cmd, verbose), cmds))
         fd, tmp = tempfile.mkstemp(suffix=".so", dir=HERE)
         os.close(fd)
         try:
             _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-pthread",
-                  host_o, dev_o, "-o", tmp], verbose)
+                  host_o, *dev_o, "-o", tmp], verbose)
             os.replace(tmp, LIB)
         finally:
             if os.path.exists(tmp):

@@ -1,0 +1,671 @@
+// Attention over the key/value cache in 4 bits.
+//
+// Query rows of a sequence that share a kv head (tokens x q heads of the kv
+// head, row = token * heads + head) run together.  For a row q and slot t with
+// pairs (lo, s) and codes u per group g of channels,
+//   q . k_t = sum_g  s_{t,g} (q . u_t)_g + lo_{t,g} (sum of q over g),
+// so the codes go into the matrix instruction as they are (see codes8) and the
+// pairs meet the 32-bit sums; likewise with probabilities p_t
+//   out_c = sum_t (p_t s_{t,g(c)}) u_{t,c} + sum_t p_t lo_{t,g(c)}.
+// One pass over the slots with a running reference r per row, p_t = 2^(z_t - r)
+// (z in binary orders: scale log2 e folded in), and the sums of p, p lo and
+// p s u in binary32; they are multiplied by 2^(old r - new r) when r moves.
+#include "stagq_kv_host.h"
+
+namespace stagq {
+namespace kv {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kNone = -1e30f;  // reference of a row that has seen nothing
+constexpr int kMaxChunkBlocks = 256;  // 64 blocks per wave (one page-table entry per lane) x 4 waves
+constexpr int kRowTile = 16;
+constexpr int kBigTile = 128;    // rows of a workgroup of attend_tiles
+
+struct AttnParams {
+  Cache c;
+  Tensor q, out;
+  const int* q_lens;
+  float* lse;
+  float* weights;
+  int64_t wsb, wsh;
+  float* part;      // [batch][kv head][split][row][D] sums, then [..][row][2] (reference, sum of p)
+  float* part_rl;
+  float scale2;     // scale * log2 e
+  int gq;           // q heads per kv head
+  int causal, window;
+  int64_t max_len;
+  int chunk;        // slots of a split
+  int nsplit, tiles, tile_rows;
+  int rows;         // tokens * gq
+};
+
+// What a sequence and a tile of rows see: slots [lo, hi), lo down to a block.
+struct Span {
+  int64_t len;
+  int ql, rows;     // query tokens and rows of the sequence
+  int64_t lo, hi;
+};
+__device__ __forceinline__ void seq_span(const AttnParams& p, int b, Span& s) {
+  const int64_t len = p.c.lengths[b];
+  s.len = len < 0 ? 0 : len > p.max_len ? p.max_len : len;
+  s.ql = p.q_lens ? min(max(p.q_lens[b], 0), p.q.tokens) : p.q.tokens;
+  s.rows = s.ql * p.gq;
+}
+__device__ __forceinline__ void tile_span(const AttnParams& p, int row0, Span& s) {
+  const int last = min(row0 + p.tile_rows, s.rows) - 1;
+  const int64_t first_pos = s.len - s.ql + row0 / p.gq, last_pos = s.len - s.ql + last / p.gq;
+  s.hi = p.causal ? max(min(last_pos + 1, s.len), int64_t(0)) : s.len;
+  s.lo = p.window > 0 ? max(first_pos - p.window + 1, int64_t(0)) & ~int64_t(kBlock - 1) : 0;
+}
+__device__ __forceinline__ int used_splits(const AttnParams& p, const Span& s) {
+  return s.hi <= s.lo ? 0 : int((s.hi - s.lo + p.chunk - 1) / p.chunk);
+}
+// Slots [from, to) that a row sees.
+__device__ __forceinline__ void row_span(const AttnParams& p, const Span& s, int row, int64_t& from, int64_t& to) {
+  const int64_t pos = s.len - s.ql + row / p.gq;
+  to = p.causal ? min(pos + 1, s.len) : s.len;
+  from = p.window > 0 ? max(pos - p.window + 1, int64_t(0)) : 0;
+}
+
+__device__ __forceinline__ const uint8_t* q_row(const AttnParams& p, int b, int hk, int row) {
+  const int t = row / p.gq, h = hk * p.gq + row - t * p.gq;
+  return p.q.data + (b * p.q.sb + t * p.q.st + h * p.q.sh) * 2;
+}
+__device__ __forceinline__ uint16_t* out_row(const AttnParams& p, int b, int hk, int row) {
+  const int t = row / p.gq, h = hk * p.gq + row - t * p.gq;
+  return reinterpret_cast<uint16_t*>(p.out.data) + (b * p.out.sb + t * p.out.st + h * p.out.sh);
+}
+__device__ __forceinline__ void put_lse(const AttnParams& p, int b, int hk, int row, float ref, float sum) {
+  const int t = row / p.gq, h = hk * p.gq + row - t * p.gq;
+  const float v = sum == 0.0f ? -__builtin_inff() : (ref + __log2f(sum)) * kLn2;
+  p.lse[(int64_t(b) * p.q.tokens + t) * p.q.heads + h] = v;
+}
+__device__ __forceinline__ int64_t part_row(const AttnParams& p, int b, int hk, int split, int row) {
+  return ((int64_t(b) * p.c.heads + hk) * p.nsplit + split) * p.rows + row;
+}
+
+// A lane's share of a 16-row query tile as the second operand of the product
+// (row n = lane & 15, channels 32 ks + 8 (lane >> 4) + e), scaled by a power of
+// two per row (see row_scale); *unit undoes it.
+template <int D>
+__device__ __forceinline__ void load_q(const AttnParams& p, int b, int hk, int row, bool there, h8_t* qf, float* unit) {
+  const int set = (threadIdx.x & 63) >> 4;
+  float f[D / 32][8];
+  float amax = 0.0f;
+  const uint8_t* src = there ? q_row(p, b, hk, row) : nullptr;
+#pragma unroll
+  for (int ks = 0; ks < D / 32; ks++) {
+    if (there) {
+      unpack8(src + (32 * ks + 8 * set) * 2, p.q.dtype, f[ks]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; e++) f[ks][e] = 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e++) amax = fmaxf(amax, fabsf(f[ks][e]));
+  }
+  const float m = row_scale(max_sets(amax));
+  *unit = 1.0f / m;
+#pragma unroll
+  for (int ks = 0; ks < D / 32; ks++)
+#pragma unroll
+    for (int e = 0; e < 8; e++) qf[ks][e] = (_Float16)(f[ks][e] * m);
+}
+
+template <int N>
+struct Chunk;
+template <> struct Chunk<1> { typedef uint32_t type; };
+template <> struct Chunk<2> { typedef u2_t type; };
+template <> struct Chunk<3> { struct type { uint32_t v[3]; __device__ uint32_t operator[](int i) const { return v[i]; } }; };
+template <> struct Chunk<4> { typedef u4_t type; };
+
+// A lane's share of one 32-token block: codes and pairs, straight from memory.
+template <int D, int G>
+struct BlockRegs {
+  static constexpr int NK = D / 32, NV = D / 16, CK = kchunk(D), CV = vchunk(D);
+  typename Chunk<CK>::type k[2][NK / CK];
+  typename Chunk<CV>::type v[NV / CV];
+  u4_t kp[2][G];   // pairs of tokens 4 set .. 4 set + 3 of each unit
+  u4_t vs[G], vl[G];
+  __device__ __forceinline__ void load(const uint8_t* base, int lane) {
+    const int set = lane >> 4;
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int g = 0; g < G; g++) kp[u][g] = *reinterpret_cast<const u4_t*>(base + kpair_at(G, 16 * u + 4 * set, g));
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int i = 0; i < NK / CK; i++)
+        k[u][i] = *reinterpret_cast<const typename Chunk<CK>::type*>(base + kcode_at(D, G, u, lane, i * CK));
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+      vs[g] = *reinterpret_cast<const u4_t*>(base + vstep_at(G, set, 0, g));
+      vl[g] = *reinterpret_cast<const u4_t*>(base + vstep_at(G, set, 0, g) + 16);
+    }
+#pragma unroll
+    for (int i = 0; i < NV / CV; i++)
+      v[i] = *reinterpret_cast<const typename Chunk<CV>::type*>(base + vcode_at(D, G, lane, i * CV));
+  }
+};
+
+// ------------------------------------------------- few rows per kv head ----
+// A tile is NQ x 16 rows; a workgroup of four waves takes one split of the
+// slots, its waves every fourth block of 32.  A wave holds its rows' q and sums
+// in registers; a block's codes come straight from memory into operand
+// registers (no LDS), requested one block ahead.
+template <int D, int G, int NQ>
+__global__ void __launch_bounds__(256) attend_rows(const AttnParams p) {
+  constexpr int NK = D / 32, NV = D / 16, KG = NK / G, VG = NV / G, NW = 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, set = lane >> 4;
+  unsigned id = blockIdx.x;
+  const int split = int(id % unsigned(p.nsplit)); id /= unsigned(p.nsplit);
+  const int tile = int(id % unsigned(p.tiles)); id /= unsigned(p.tiles);
+  const int hk = int(id % unsigned(p.c.heads)), b = int(id / unsigned(p.c.heads));
+  Span s;
+  seq_span(p, b, s);
+  const int row0 = tile * NQ * kRowTile;
+  if (row0 >= s.rows) return;
+  tile_span(p, row0, s);
+  const int used = used_splits(p, s);
+  if (split >= used && split > 0) return;   // split 0 writes the zeros of a tile that sees nothing
+  const int64_t begin = s.lo + int64_t(split) * p.chunk, end = min(begin + p.chunk, s.hi);
+  const int nblk = end > begin ? int((end - begin + kBlock - 1) / kBlock) : 0;
+  const int mine = nblk > wave ? (nblk - wave + NW - 1) / NW : 0;
+
+  // lane i holds the page of the wave's block i
+  int page = -1;
+  {
+    const int64_t slot = begin + int64_t(wave + lane * NW) * kBlock;
+    const int64_t e = slot >> p.c.shift;
+    if (lane < mine && e < p.c.width) page = p.c.table[int64_t(b) * p.c.table_stride + e];
+    if (page >= p.c.pages) page = -1;
+  }
+  const int64_t in_page = (int64_t(1) << p.c.shift) - 1;
+  auto where = [&](int i) -> const uint8_t* {
+    const int pg = __builtin_amdgcn_readlane(page, i);
+    if (pg < 0) return nullptr;
+    const int64_t slot = begin + int64_t(wave + i * NW) * kBlock;
+    return p.c.buf + uint64_t(pg) * p.c.page_bytes + uint64_t(hk) * p.c.head_bytes +
+           uint32_t((slot & in_page) / kBlock) * block_bytes(D, G);
+  };
+
+  BlockRegs<D, G> cur, nxt;
+  const uint8_t* at = mine > 0 ? where(0) : nullptr;
+  if (at) cur.load(at, lane);
+
+  h8_t qf[NQ][NK];
+  float qsum[NQ][G], z_unit[NQ], ref[NQ], top[NQ], psum[NQ], plo[NQ][G];
+  int64_t from[NQ], to[NQ];
+  f4_t acc[NQ][NV];
+#pragma unroll
+  for (int t = 0; t < NQ; t++) {
+    const int row = row0 + t * kRowTile + n;
+    const bool there = row < s.rows;
+    float unit;
+    load_q<D>(p, b, hk, row, there, qf[t], &unit);
+    z_unit[t] = p.scale2 * kCodeUnit * unit;
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+      float a = 0.0f;
+#pragma unroll
+      for (int ks = g * KG; ks < (g + 1) * KG; ks++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) a += (float)qf[t][ks][e];
+      qsum[t][g] = sum_sets(a) * (1.0f / kCodeUnit);
+      plo[t][g] = 0.0f;
+    }
+    from[t] = to[t] = 0;
+    if (there) row_span(p, s, row, from[t], to[t]);
+    ref[t] = top[t] = kNone;
+    psum[t] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NV; c++) acc[t][c] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  // slots that every row of the tile sees: [all_from, all_to)
+  int64_t all_from = 0, all_to = s.len;
+  {
+    int64_t f, t;
+    row_span(p, s, row0, f, t);
+    all_to = t;
+    row_span(p, s, min(row0 + NQ * kRowTile, s.rows) - 1, f, t);
+    all_from = f;
+  }
+  // p s goes into fp16: the reference lies `lift` below the row's largest z, so
+  // that the largest step seen times 2^lift is near 2^8 (limit 2^15).  Then a
+  // product is lost only 2^-33 below the largest, whatever the scale of V.
+  float lift = 0.0f, s_limit = -1.0f;
+
+  for (int i = 0; i < mine; i++) {
+    const uint8_t* ahead = i + 1 < mine ? where(i + 1) : nullptr;
+    if (ahead) nxt.load(ahead, lane);
+    if (at) {
+      const int64_t slot0 = begin + int64_t(wave + i * NW) * kBlock;
+      const bool whole = slot0 >= all_from && slot0 + kBlock <= all_to;
+      if (!whole) {   // pairs of slots that hold nothing yet may be anything
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+          if (slot0 + vtoken(set, e) >= s.len)
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+              const uint32_t keep = (e & 1) ? 0x0000ffffu : 0xffff0000u;
+              cur.vs[g][e / 2] &= keep;
+              cur.vl[g][e / 2] &= keep;
+            }
+      }
+      float smax = 0.0f;
+      {
+        h2_t m = {(_Float16)0.0f, (_Float16)0.0f};
+#pragma unroll
+        for (int g = 0; g < G; g++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) m = __builtin_elementwise_max(m, __builtin_bit_cast(h2_t, (uint32_t)cur.vs[g][e]));
+        smax = fmaxf((float)m[0], (float)m[1]);
+      }
+      float z[NQ][8];
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        h8_t kf[NK];
+#pragma unroll
+        for (int ks = 0; ks < NK; ks++) kf[ks] = codes8(cur.k[u][ks / BlockRegs<D, G>::CK][ks % BlockRegs<D, G>::CK]);
+#pragma unroll
+        for (int t = 0; t < NQ; t++) {
+          float zz[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int g = 0; g < G; g++) {
+            f4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int ks = g * KG; ks < (g + 1) * KG; ks++)
+              a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[ks], qf[t][ks], a, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+              const h2_t pair = __builtin_bit_cast(h2_t, (uint32_t)cur.kp[u][g][r]);
+              zz[r] = fmaf((float)pair[1], a[r], zz[r]);
+              zz[r] = fmaf((float)pair[0], qsum[t][g], zz[r]);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 4; r++) z[t][u * 4 + r] = zz[r] * z_unit[t];
+        }
+      }
+      if (!whole) {
+#pragma unroll
+        for (int t = 0; t < NQ; t++)
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            const int64_t slot = slot0 + vtoken(set, e);
+            z[t][e] = slot >= from[t] && slot < to[t] ? z[t][e] : -__builtin_inff();
+          }
+      }
+      bool moves = smax > s_limit;
+      float mx[NQ];
+#pragma unroll
+      for (int t = 0; t < NQ; t++) {
+        mx[t] = fmaxf(fmaxf(fmaxf(z[t][0], z[t][1]), fmaxf(z[t][2], z[t][3])),
+                      fmaxf(fmaxf(z[t][4], z[t][5]), fmaxf(z[t][6], z[t][7])));
+        moves |= mx[t] > top[t];
+      }
+      if (__any(moves)) {   // rare: the reference of some row moves
+        float sm = max_sets(smax);
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2) sm = fmaxf(sm, __shfl_xor(sm, d));
+        if (sm > s_limit) {
+          int e = (__builtin_bit_cast(int, fmaxf(sm, 5.9604645e-8f)) >> 23) - 127;   // 2^e <= sm
+          lift = float(8 - e);
+          s_limit = exp2_fast(float(e + 7));
+        }
+#pragma unroll
+        for (int t = 0; t < NQ; t++) {
+          top[t] = fmaxf(top[t], max_sets(mx[t]));
+          const float r = top[t] - lift, f = exp2_fast(ref[t] - r);
+          ref[t] = r;
+          psum[t] *= f;
+#pragma unroll
+          for (int g = 0; g < G; g++) plo[t][g] *= f;
+#pragma unroll
+          for (int c = 0; c < NV; c++) acc[t][c] *= f;
+        }
+      }
+      h8_t pf[NQ][G];
+#pragma unroll
+      for (int t = 0; t < NQ; t++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const float pe = exp2_fast(z[t][e] - ref[t]);
+          psum[t] += pe;
+#pragma unroll
+          for (int g = 0; g < G; g++) {
+            const h8_t sv = __builtin_bit_cast(h8_t, cur.vs[g]), lv = __builtin_bit_cast(h8_t, cur.vl[g]);
+            plo[t][g] = fmaf(pe, (float)lv[e], plo[t][g]);
+            pf[t][g][e] = (_Float16)(pe * (float)sv[e]);   // one rounding to 11 bits per product
+          }
+        }
+#pragma unroll
+      for (int c = 0; c < NV; c++) {
+        const h8_t vf = codes8(cur.v[c / BlockRegs<D, G>::CV][c % BlockRegs<D, G>::CV]);
+#pragma unroll
+        for (int t = 0; t < NQ; t++)
+          acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[t][c / VG], acc[t][c], 0, 0, 0);
+      }
+    }
+    cur = nxt;
+    at = ahead;
+  }
+
+  // Join the four waves in LDS, in a fixed order.
+  constexpr int LD = D + 4;
+  __shared__ float sums[NW][kRowTile][LD];
+  __shared__ float refs[NW][kRowTile], ls[NW][kRowTile];
+  for (int t = 0; t < NQ; t++) {
+    if (t) __syncthreads();
+    const float l = sum_sets(psum[t]);
+    float lo[G];
+#pragma unroll
+    for (int g = 0; g < G; g++) lo[g] = sum_sets(plo[t][g]);
+#pragma unroll
+    for (int c = 0; c < NV; c++) {
+      f4_t o;
+#pragma unroll
+      for (int r = 0; r < 4; r++) o[r] = fmaf(acc[t][c][r], kCodeUnit, lo[c / VG]);
+      *reinterpret_cast<f4_t*>(&sums[wave][n][16 * c + 4 * set]) = o;
+    }
+    if (set == 0) { refs[wave][n] = ref[t]; ls[wave][n] = l; }
+    __syncthreads();
+    for (int it = threadIdx.x; it < kRowTile * (D / 4); it += 256) {
+      const int r = it / (D / 4), c = (it % (D / 4)) * 4, row = row0 + t * kRowTile + r;
+      if (row >= s.rows) continue;
+      float m = refs[0][r], l2 = 0.0f;
+#pragma unroll
+      for (int w = 1; w < NW; w++) m = fmaxf(m, refs[w][r]);
+      f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < NW; w++) {
+        const float f = exp2_fast(refs[w][r] - m);
+        l2 = fmaf(ls[w][r], f, l2);
+        const f4_t x = *reinterpret_cast<const f4_t*>(&sums[w][r][c]);
+        o += x * f;
+      }
+      if (p.nsplit == 1) {
+        const float inv = l2 == 0.0f ? 0.0f : 1.0f / l2;
+        u2_t w2;
+        w2[0] = uint32_t(to_16(o[0] * inv, p.q.dtype)) | uint32_t(to_16(o[1] * inv, p.q.dtype)) << 16;
+        w2[1] = uint32_t(to_16(o[2] * inv, p.q.dtype)) | uint32_t(to_16(o[3] * inv, p.q.dtype)) << 16;
+        *reinterpret_cast<u2_t*>(out_row(p, b, hk, row) + c) = w2;
+        if (p.lse && c == 0) put_lse(p, b, hk, row, m, l2);
+      } else if (split < used) {
+        const int64_t at_row = part_row(p, b, hk, split, row);
+        *reinterpret_cast<f4_t*>(p.part + at_row * D + c) = o;
+        if (c == 0) { p.part_rl[at_row * 2] = m; p.part_rl[at_row * 2 + 1] = l2; }
+      }
+    }
+  }
+}
+
+// Join the splits of a row, in their order: one wave per row.
+template <int D>
+__global__ void __launch_bounds__(64) join_kernel(const AttnParams p) {
+  constexpr int PER = D / 32;   // channels per lane of half a wave
+  unsigned id = blockIdx.x;
+  const int row = int(id % unsigned(p.rows)); id /= unsigned(p.rows);
+  const int hk = int(id % unsigned(p.c.heads)), b = int(id / unsigned(p.c.heads));
+  Span s;
+  seq_span(p, b, s);
+  if (row >= s.rows) return;
+  tile_span(p, row / p.tile_rows * p.tile_rows, s);
+  const int used = used_splits(p, s);
+  const int lane = threadIdx.x, half = lane >> 5, c = (lane & 31) * PER;
+  float m = kNone;
+  for (int i = lane; i < used; i += 64) m = fmaxf(m, p.part_rl[part_row(p, b, hk, i, row) * 2]);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+  float l = 0.0f, o[PER] = {};
+  for (int i = half; i < used; i += 2) {   // even splits in one half of the wave, odd ones in the other
+    const int64_t at = part_row(p, b, hk, i, row);
+    const float f = exp2_fast(p.part_rl[at * 2] - m);
+    l = fmaf(p.part_rl[at * 2 + 1], f, l);
+#pragma unroll
+    for (int k = 0; k < PER; k++) o[k] = fmaf(p.part[at * D + c + k], f, o[k]);
+  }
+  l += __shfl_xor(l, 32);
+#pragma unroll
+  for (int k = 0; k < PER; k++) o[k] += __shfl_xor(o[k], 32);
+  if (half == 0) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t* dst = out_row(p, b, hk, row) + c;
+#pragma unroll
+    for (int k = 0; k < PER; k++) dst[k] = to_16(o[k] * inv, p.q.dtype);
+    if (p.lse && lane == 0) put_lse(p, b, hk, row, m, l);
+  }
+}
+
+// Weight of every cached slot: the sum of P over the sequence's rows, from the
+// rows' log-sum-exp.  A wave owns one block of 32 slots, so no two waves add to
+// one slot and the order of the sums is fixed.
+template <int D, int G>
+__global__ void __launch_bounds__(256) weigh_kernel(const AttnParams p) {
+  constexpr int NK = D / 32, KG = NK / G, CK = kchunk(D);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, set = lane >> 4;
+  unsigned id = blockIdx.x;
+  const unsigned per = unsigned((p.max_len + 4 * kBlock - 1) / (4 * kBlock));
+  const int64_t slot0 = (int64_t(id % per) * 4 + wave) * kBlock; id /= per;
+  const int hk = int(id % unsigned(p.c.heads)), b = int(id / unsigned(p.c.heads));
+  Span s;
+  seq_span(p, b, s);
+  if (slot0 >= s.len || s.rows == 0) return;
+  const uint8_t* base = block_at<D, G>(p.c, b, hk, slot0);
+  if (!base) return;
+  h8_t kf[2][NK];
+  u4_t kp[2][G];
+#pragma unroll
+  for (int u = 0; u < 2; u++) {
+#pragma unroll
+    for (int g = 0; g < G; g++) kp[u][g] = *reinterpret_cast<const u4_t*>(base + kpair_at(G, 16 * u + 4 * set, g));
+#pragma unroll
+    for (int i = 0; i < NK / CK; i++) {
+      const auto w = *reinterpret_cast<const typename Chunk<CK>::type*>(base + kcode_at(D, G, u, lane, i * CK));
+#pragma unroll
+      for (int x = 0; x < CK; x++) {
+        if constexpr (CK == 1) kf[u][i] = codes8(w);
+        else kf[u][i * CK + x] = codes8(w[x]);
+      }
+    }
+  }
+  float sum[8] = {};
+  const float* lse = p.lse + int64_t(b) * p.q.tokens * p.q.heads;
+  for (int row0 = 0; row0 < s.rows; row0 += kRowTile) {
+    const int row = row0 + n;
+    const bool there = row < s.rows;
+    int64_t from = 0, to = 0;
+    if (there) row_span(p, s, row, from, to);
+    if (!__any(from < slot0 + kBlock && to > slot0)) continue;
+    h8_t qf[NK];
+    float unit;
+    load_q<D>(p, b, hk, row, there, qf, &unit);
+    const float z_unit = p.scale2 * kCodeUnit * unit;
+    const int t = row / p.gq;
+    const float l = there ? lse[int64_t(t) * p.q.heads + hk * p.gq + row - t * p.gq] : 0.0f;
+    const float l2 = l * kLog2e;
+    float z[8] = {};
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+      float qs = 0.0f;
+#pragma unroll
+      for (int ks = g * KG; ks < (g + 1) * KG; ks++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) qs += (float)qf[ks][e];
+      qs = sum_sets(qs) * (1.0f / kCodeUnit);
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        f4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int ks = g * KG; ks < (g + 1) * KG; ks++)
+          a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u][ks], qf[ks], a, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+          const h2_t pair = __builtin_bit_cast(h2_t, (uint32_t)kp[u][g][r]);
+          z[u * 4 + r] = fmaf((float)pair[1], a[r], z[u * 4 + r]);
+          z[u * 4 + r] = fmaf((float)pair[0], qs, z[u * 4 + r]);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      const int64_t slot = slot0 + vtoken(set, e);
+      sum[e] += slot >= from && slot < to ? exp2_fast(z[e] * z_unit - l2) : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; e++)
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) sum[e] += __shfl_xor(sum[e], d);
+  if (n == 0) {
+    float* w = p.weights + b * p.wsb + hk * p.wsh;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      const int64_t slot = slot0 + vtoken(set, e);
+      if (slot < s.len) w[slot] += sum[e];
+    }
+  }
+}
+
+// ------------------------------------------------------------- dispatch ----
+struct Plan {
+  int nq, tile_rows, tiles, chunk, nsplit;
+  int64_t groups;
+  size_t part, rl, lse, total;   // workspace: floats of the sums, offsets in bytes
+};
+
+// Variants and splits by shape alone.
+static bool plan(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_attn* a, Plan* pl) {
+  const int gq = a->q.heads / c->kv_heads;
+  const int64_t rows = int64_t(a->q.tokens) * gq;
+  if (rows > (int64_t(1) << 30)) return false;
+  pl->nq = rows > kRowTile ? 2 : 1;
+  pl->tile_rows = pl->nq * kRowTile;
+  pl->tiles = int((rows + pl->tile_rows - 1) / pl->tile_rows);
+  int64_t span = reach(c, q, a->max_len);
+  if (a->window > 0) {   // a tile's rows see at most this many slots, from a block's start
+    const int64_t most = int64_t(a->window) + (pl->tile_rows + gq - 1) / gq + 1 + kBlock;
+    span = most < span ? most : span;
+  }
+  const int64_t blocks = (span + kBlock - 1) / kBlock;
+  const int64_t base = int64_t(q->batch) * c->kv_heads * pl->tiles;
+  const int64_t wanted = base > 0 ? (1024 + base - 1) / base : 1;
+  int64_t per = (blocks + wanted - 1) / wanted;
+  per = per < 8 ? 8 : per > kMaxChunkBlocks ? kMaxChunkBlocks : per;
+  per = (per + 3) / 4 * 4;
+  pl->chunk = int(per) * kBlock;
+  pl->nsplit = int(blocks ? (blocks + per - 1) / per : 1);
+  pl->groups = base * pl->nsplit;
+  if (!launchable(pl->groups, 256)) return false;
+  const size_t rows_all = size_t(q->batch) * c->kv_heads * pl->nsplit * size_t(rows);
+  size_t o = 0;
+  pl->part = o;
+  if (pl->nsplit > 1) o += (rows_all * c->head_dim * 4 + 255) / 256 * 256;
+  pl->rl = o;
+  if (pl->nsplit > 1) o += (rows_all * 8 + 255) / 256 * 256;
+  pl->lse = o;
+  if (a->weights && !a->lse) o += (size_t(q->batch) * a->q.tokens * a->q.heads * 4 + 255) / 256 * 256;
+  pl->total = o;
+  return true;
+}
+
+struct LaunchAttention {
+  AttnParams p;
+  Plan pl;
+  hipStream_t st;
+  template <int D, int G>
+  int go() {
+    const dim3 grid((unsigned)pl.groups);
+    if (pl.nq == 1) hipLaunchKernelGGL((attend_rows<D, G, 1>), grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((attend_rows<D, G, 2>), grid, dim3(256), 0, st, p);
+    int s = launched();
+    if (s != STAGQ_OK) return s;
+    if (p.nsplit > 1) {
+      const int64_t n = int64_t(p.c.batch) * p.c.heads * p.rows;
+      hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)n), dim3(64), 0, st, p);
+      s = launched();
+      if (s != STAGQ_OK) return s;
+    }
+    if (p.weights && p.max_len > 0) {
+      const int64_t per = (p.max_len + 4 * kBlock - 1) / (4 * kBlock);
+      const int64_t n = per * p.c.batch * p.c.heads;
+      hipLaunchKernelGGL((weigh_kernel<D, G>), dim3((unsigned)n), dim3(256), 0, st, p);
+      s = launched();
+    }
+    return s;
+  }
+};
+
+static int check_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_attn* a) {
+  int st = check_cache(c);
+  if (st == STAGQ_OK) st = check_seqs(q);
+  if (st != STAGQ_OK) return st;
+  if (!a) return STAGQ_EINVAL;
+  if (a->q.heads < 1 || a->q.heads % c->kv_heads) return STAGQ_ESHAPE;
+  st = check_tensor(a->q, a->q.heads, false, q->batch);
+  if (st == STAGQ_OK) st = check_tensor(a->out, a->q.heads, false, q->batch);
+  if (st != STAGQ_OK) return st;
+  if (a->q.dtype != a->out.dtype || a->q.tokens != a->out.tokens) return STAGQ_EINVAL;
+  if (a->window < 0 || (a->window > 0 && !a->causal) || a->max_len < 0) return STAGQ_EINVAL;
+  if (!(a->scale - a->scale == 0.0f)) return STAGQ_EINVAL;   // infinite or NaN
+  if (misaligned(a->q_lens, 4) || misaligned(a->lse, 4) || misaligned(a->weights, 4)) return STAGQ_EALIGN;
+  if (a->weights && (a->weights_stride_seq < 0 || a->weights_stride_head < 0)) return STAGQ_EINVAL;
+  const int64_t groups = (reach(c, q, a->max_len) + 4 * kBlock - 1) / (4 * kBlock) * q->batch * c->kv_heads;
+  if (a->weights && !launchable(groups, 256)) return STAGQ_ESHAPE;
+  if (!launchable(int64_t(q->batch) * a->q.tokens * a->q.heads, 64)) return STAGQ_ESHAPE;
+  return STAGQ_OK;
+}
+
+}  // namespace kv
+}  // namespace stagq
+
+using namespace stagq::kv;
+
+extern "C" {
+
+size_t stagq_kv_attention_workspace(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_attn* a) {
+  Plan pl;
+  if (check_attention(c, q, a) != STAGQ_OK || !plan(c, q, a, &pl)) return 0;
+  return pl.total;
+}
+
+int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_attn* a, void* workspace,
+                       size_t workspace_bytes, void* hip_stream) {
+  const int st = check_attention(c, q, a);
+  if (st != STAGQ_OK) return st;
+  if (q->batch == 0 || a->q.tokens == 0) return STAGQ_OK;
+  Plan pl;
+  if (!plan(c, q, a, &pl)) return STAGQ_ESHAPE;
+  if (pl.total > 0 && !workspace) return STAGQ_EINVAL;
+  if (misaligned(workspace, 256)) return STAGQ_EALIGN;
+  if (workspace_bytes < pl.total) return STAGQ_ESIZE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  AttnParams p;
+  p.c = make_cache(c, q);
+  p.q = make_tensor(a->q);
+  p.out = make_tensor(a->out);
+  p.q_lens = a->q_lens;
+  p.lse = a->lse ? a->lse : a->weights ? reinterpret_cast<float*>(ws + pl.lse) : nullptr;
+  p.weights = a->weights;
+  p.wsb = a->weights_stride_seq;
+  p.wsh = a->weights_stride_head;
+  p.part = reinterpret_cast<float*>(ws + pl.part);
+  p.part_rl = reinterpret_cast<float*>(ws + pl.rl);
+  p.scale2 = a->scale * kLog2e;
+  p.gq = a->q.heads / c->kv_heads;
+  p.causal = a->causal != 0;
+  p.window = a->window;
+  p.max_len = reach(c, q, a->max_len);
+  p.chunk = pl.chunk;
+  p.nsplit = pl.nsplit;
+  p.tiles = pl.tiles;
+  p.tile_rows = pl.tile_rows;
+  p.rows = a->q.tokens * p.gq;
+  return by_shape(c, LaunchAttention{p, pl, static_cast<hipStream_t>(hip_stream)});
+}
+
+}  // extern "C"

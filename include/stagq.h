@@ -373,10 +373,11 @@ int stagq_kv_append(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq
 /*
  * The values the cache holds, lo + s u rounded once to the tensors' type: row i
  * of k and v receives slot start[b] + i (start NULL: slot i) where that is
- * below lengths[b]; other rows are left as they were.
+ * in 0 .. lengths[b] - 1; other rows are left as they were, or with zero_rest
+ * set to 0.
  */
 int stagq_kv_read(const stagq_kv_cache* c, const stagq_kv_seqs* q, const int32_t* start,
-                  const stagq_kv_tensor* k, const stagq_kv_tensor* v, void* hip_stream);
+                  const stagq_kv_tensor* k, const stagq_kv_tensor* v, int zero_rest, void* hip_stream);
 
 /*
  * Attention of query rows over the cache.  Row i < q_lens[b] (clamped to
@@ -392,8 +393,9 @@ int stagq_kv_read(const stagq_kv_cache* c, const stagq_kv_seqs* q, const int32_t
  *            sequence's rows and the q heads of h
  *   max_len  bound of the lengths that sizes the launch (0: the table's width);
  *            a longer sequence is cut to it
- * Rows from q_lens[b] on are neither read nor written in q, out and lse.  q and
- * out are fp16 or bf16, both the same.
+ *   zero_rest  not 0: rows of out from q_lens[b] on are set to 0
+ * Rows from q_lens[b] on are not read in q, and not written in lse and (without
+ * zero_rest) out.  q and out are fp16 or bf16, both the same.
  */
 typedef struct {
   stagq_kv_tensor q, out;
@@ -403,6 +405,7 @@ typedef struct {
   int64_t weights_stride_seq, weights_stride_head;
   float scale;
   int32_t causal, window, max_len;
+  int32_t zero_rest, spare;
 } stagq_kv_attn;
 
 /* Bytes of device workspace (256-byte aligned) the call needs; it holds nothing

@@ -21,12 +21,19 @@ import numpy as np
 
 from . import _lib as _lib_mod
 from ._lib import EXPORTED, Info, StagQError, check, fields_struct, lib  # noqa: F401
-from .kv_cache import KVCache  # noqa: F401
 
 
 def load() -> None:
     """Load libstagq.so now (raises ImportError if it has not been built)."""
     lib()
+
+
+def __getattr__(name):
+    if name == "KVCache":   # its module imports torch, which hosts that only encode and pack do without
+        from .kv_cache import KVCache
+        return KVCache
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 __all__ = ["StagQMatrix", "KVCache", "encode", "pack_host", "unpack_host", "packed_bytes", "plan_gemv",
            "StagQError"]

@@ -47,45 +47,6 @@ class Info(C.Structure):
     ]
 
 
-class KvCache(C.Structure):
-    _fields_ = [
-        ("pages", C.c_int32), ("page_tokens", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
-        ("group", C.c_int32), ("spare", C.c_int32), ("buf", C.c_void_p), ("bytes", C.c_uint64),
-    ]
-
-
-class KvSeqs(C.Structure):
-    _fields_ = [
-        ("batch", C.c_int32), ("table_width", C.c_int32), ("table_stride", C.c_int64), ("table", C.c_void_p),
-        ("lengths", C.c_void_p),
-    ]
-
-
-class KvTensor(C.Structure):
-    _fields_ = [
-        ("data", C.c_void_p), ("dtype", C.c_int32), ("tokens", C.c_int32), ("heads", C.c_int32),
-        ("spare", C.c_int32), ("stride_seq", C.c_int64), ("stride_token", C.c_int64), ("stride_head", C.c_int64),
-    ]
-
-
-class KvAttn(C.Structure):
-    _fields_ = [
-        ("q", KvTensor), ("out", KvTensor), ("q_lens", C.c_void_p), ("lse", C.c_void_p), ("weights", C.c_void_p),
-        ("weights_stride_seq", C.c_int64), ("weights_stride_head", C.c_int64), ("scale", C.c_float),
-        ("causal", C.c_int32), ("window", C.c_int32), ("max_len", C.c_int32),
-    ]
-
-
-class KvEvict(C.Structure):
-    _fields_ = [
-        ("weights", C.c_void_p), ("weights_out", C.c_void_p), ("weights_stride_seq", C.c_int64),
-        ("weights_stride_head", C.c_int64), ("out_stride_seq", C.c_int64), ("out_stride_head", C.c_int64),
-        ("kept", C.c_void_p), ("out_lengths", C.c_void_p), ("out_table", C.c_void_p),
-        ("out_table_stride", C.c_int64), ("out_table_width", C.c_int32), ("keep", C.c_int32), ("sinks", C.c_int32),
-        ("recent", C.c_int32), ("max_len", C.c_int32), ("spare", C.c_int32),
-    ]
-
-
 def _load() -> C.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -112,10 +73,10 @@ def _load() -> C.CDLL:
                                       C.c_int, P]),
         "stagq_stream_read": (C.c_int, [P, C.c_size_t, P, P]),
         "stagq_stream_read_shape": (C.c_int, [P, C.c_size_t, P, C.c_int, C.c_int, C.c_int, P]),
-        # the key/value cache: structs by address
+        # the key/value cache: structs by address, packed in kv_cache.py
         "stagq_kv_bytes": (C.c_size_t, [P]),
         "stagq_kv_append": (C.c_int, [P, P, P, P, P, P]),
-        "stagq_kv_read": (C.c_int, [P, P, P, P, P, P]),
+        "stagq_kv_read": (C.c_int, [P, P, P, P, P, C.c_int, P]),
         "stagq_kv_attention_workspace": (C.c_size_t, [P, P, P]),
         "stagq_kv_attention": (C.c_int, [P, P, P, P, C.c_size_t, P]),
         "stagq_kv_evict_workspace": (C.c_size_t, [P, P, P]),

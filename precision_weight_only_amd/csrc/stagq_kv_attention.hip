@@ -18,9 +18,10 @@ namespace kv {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNone = -1e30f;  // reference of a row that has seen nothing
-constexpr int kMaxChunkBlocks = 256;  // 64 blocks per wave (one page-table entry per lane) x 4 waves
 constexpr int kRowTile = 16;
-constexpr int kBigTile = 128;    // rows of a workgroup of attend_tiles
+constexpr int kWantedGroups = 512;  // two workgroups per CU
+constexpr int kMinBlocks = 16;      // of a split
+constexpr int kStashRows = 8;       // up to this many rows z is kept for the weights
 
 struct AttnParams {
   Cache c;
@@ -32,13 +33,21 @@ struct AttnParams {
   float* part;      // [batch][kv head][split][row][D] sums, then [..][row][2] (reference, sum of p)
   float* part_rl;
   float scale2;     // scale * log2 e
-  int gq;           // q heads per kv head
-  int causal, window;
+  unsigned gq, gq_inv;  // q heads per kv head, and floor(2^32 / gq), at most 2^32 - 1
+  int causal, window, zero_rest;
+  float* stash;     // or z (binary orders) of [batch][kv head][row][stash_len]
+  int64_t stash_len;
   int64_t max_len;
   int chunk;        // slots of a split
   int nsplit, tiles, tile_rows;
   int rows;         // tokens * gq
 };
+
+// The token of a row: row / gq, from the reciprocal, which is at most one short.
+__device__ __forceinline__ int token_of(const AttnParams& p, int row) {
+  const unsigned q = __umulhi(unsigned(row), p.gq_inv);
+  return int(unsigned(row) - q * p.gq >= p.gq ? q + 1 : q);
+}
 
 // What a sequence and a tile of rows see: slots [lo, hi), lo down to a block.
 struct Span {
@@ -50,11 +59,11 @@ __device__ __forceinline__ void seq_span(const AttnParams& p, int b, Span& s) {
   const int64_t len = p.c.lengths[b];
   s.len = len < 0 ? 0 : len > p.max_len ? p.max_len : len;
   s.ql = p.q_lens ? min(max(p.q_lens[b], 0), p.q.tokens) : p.q.tokens;
-  s.rows = s.ql * p.gq;
+  s.rows = s.ql * int(p.gq);
 }
 __device__ __forceinline__ void tile_span(const AttnParams& p, int row0, Span& s) {
   const int last = min(row0 + p.tile_rows, s.rows) - 1;
-  const int64_t first_pos = s.len - s.ql + row0 / p.gq, last_pos = s.len - s.ql + last / p.gq;
+  const int64_t first_pos = s.len - s.ql + token_of(p, row0), last_pos = s.len - s.ql + token_of(p, last);
   s.hi = p.causal ? max(min(last_pos + 1, s.len), int64_t(0)) : s.len;
   s.lo = p.window > 0 ? max(first_pos - p.window + 1, int64_t(0)) & ~int64_t(kBlock - 1) : 0;
 }
@@ -63,26 +72,40 @@ __device__ __forceinline__ int used_splits(const AttnParams& p, const Span& s) {
 }
 // Slots [from, to) that a row sees.
 __device__ __forceinline__ void row_span(const AttnParams& p, const Span& s, int row, int64_t& from, int64_t& to) {
-  const int64_t pos = s.len - s.ql + row / p.gq;
+  const int64_t pos = s.len - s.ql + token_of(p, row);
   to = p.causal ? min(pos + 1, s.len) : s.len;
   from = p.window > 0 ? max(pos - p.window + 1, int64_t(0)) : 0;
 }
 
 __device__ __forceinline__ const uint8_t* q_row(const AttnParams& p, int b, int hk, int row) {
-  const int t = row / p.gq, h = hk * p.gq + row - t * p.gq;
+  const int t = token_of(p, row), h = (hk - t) * int(p.gq) + row;
   return p.q.data + (b * p.q.sb + t * p.q.st + h * p.q.sh) * 2;
 }
 __device__ __forceinline__ uint16_t* out_row(const AttnParams& p, int b, int hk, int row) {
-  const int t = row / p.gq, h = hk * p.gq + row - t * p.gq;
+  const int t = token_of(p, row), h = (hk - t) * int(p.gq) + row;
   return reinterpret_cast<uint16_t*>(p.out.data) + (b * p.out.sb + t * p.out.st + h * p.out.sh);
 }
 __device__ __forceinline__ void put_lse(const AttnParams& p, int b, int hk, int row, float ref, float sum) {
-  const int t = row / p.gq, h = hk * p.gq + row - t * p.gq;
+  const int t = token_of(p, row), h = (hk - t) * int(p.gq) + row;
   const float v = sum == 0.0f ? -__builtin_inff() : (ref + __log2f(sum)) * kLn2;
   p.lse[(int64_t(b) * p.q.tokens + t) * p.q.heads + h] = v;
 }
 __device__ __forceinline__ int64_t part_row(const AttnParams& p, int b, int hk, int split, int row) {
   return ((int64_t(b) * p.c.heads + hk) * p.nsplit + split) * p.rows + row;
+}
+
+// Four channels of a row's result from its sums.
+__device__ __forceinline__ void put_out(const AttnParams& p, int b, int hk, int row, int c, f4_t o, float sum) {
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  u2_t w;
+  w[0] = uint32_t(to_16(o[0] * inv, p.q.dtype)) | uint32_t(to_16(o[1] * inv, p.q.dtype)) << 16;
+  w[1] = uint32_t(to_16(o[2] * inv, p.q.dtype)) | uint32_t(to_16(o[3] * inv, p.q.dtype)) << 16;
+  *reinterpret_cast<u2_t*>(out_row(p, b, hk, row) + c) = w;
+}
+template <int D>
+__device__ __forceinline__ void zero_rows(const AttnParams& p, int b, int hk, int row, int end) {
+  for (int it = threadIdx.x; it < (end - row) * (D / 4); it += blockDim.x)
+    *reinterpret_cast<u2_t*>(out_row(p, b, hk, row + it / (D / 4)) + (it % (D / 4)) * 4) = u2_t{0u, 0u};
 }
 
 // A lane's share of a 16-row query tile as the second operand of the product
@@ -115,59 +138,63 @@ __device__ __forceinline__ void load_q(const AttnParams& p, int b, int hk, int r
 
 template <int N>
 struct Chunk;
-template <> struct Chunk<1> { typedef uint32_t type; };
 template <> struct Chunk<2> { typedef u2_t type; };
 template <> struct Chunk<3> { struct type { uint32_t v[3]; __device__ uint32_t operator[](int i) const { return v[i]; } }; };
 template <> struct Chunk<4> { typedef u4_t type; };
 
-// A lane's share of one 32-token block: codes and pairs, straight from memory.
+// ------------------------------------------------- few rows per kv head ----
+// A tile is NQ x 16 rows; a workgroup takes one split of the slots, its waves
+// every NW-th block of 32.  A wave keeps its rows' q and sums in registers and
+// moves blocks through a ring of its own in LDS: the block is one contiguous
+// piece in operand order, so it is copied there by direct loads that hold no
+// registers while they are under way, DEPTH - 1 blocks ahead.  No barrier in
+// the loop: a wave waits for its own loads only.
+constexpr int ring_waves(int D) { return D == 256 ? 2 : 4; }
 template <int D, int G>
-struct BlockRegs {
-  static constexpr int NK = D / 32, NV = D / 16, CK = kchunk(D), CV = vchunk(D);
-  typename Chunk<CK>::type k[2][NK / CK];
-  typename Chunk<CV>::type v[NV / CV];
-  u4_t kp[2][G];   // pairs of tokens 4 set .. 4 set + 3 of each unit
-  u4_t vs[G], vl[G];
-  __device__ __forceinline__ void load(const uint8_t* base, int lane) {
-    const int set = lane >> 4;
-#pragma unroll
-    for (int u = 0; u < 2; u++)
-#pragma unroll
-      for (int g = 0; g < G; g++) kp[u][g] = *reinterpret_cast<const u4_t*>(base + kpair_at(G, 16 * u + 4 * set, g));
-#pragma unroll
-    for (int u = 0; u < 2; u++)
-#pragma unroll
-      for (int i = 0; i < NK / CK; i++)
-        k[u][i] = *reinterpret_cast<const typename Chunk<CK>::type*>(base + kcode_at(D, G, u, lane, i * CK));
-#pragma unroll
-    for (int g = 0; g < G; g++) {
-      vs[g] = *reinterpret_cast<const u4_t*>(base + vstep_at(G, set, 0, g));
-      vl[g] = *reinterpret_cast<const u4_t*>(base + vstep_at(G, set, 0, g) + 16);
-    }
-#pragma unroll
-    for (int i = 0; i < NV / CV; i++)
-      v[i] = *reinterpret_cast<const typename Chunk<CV>::type*>(base + vcode_at(D, G, lane, i * CV));
-  }
+struct Ring {
+  static constexpr int NW = ring_waves(D);
+  static constexpr uint32_t BB = block_bytes(D, G);
+  static constexpr int DEPTH = D == 64 ? 4 : 3;              // a workgroup's rings fit in 64 KB, two of them in a CU
+  static constexpr int LOADS = int((BB + 1023) / 1024);      // of a wave per block
+  static constexpr uint32_t BYTES = NW * DEPTH * BB;
 };
 
-// ------------------------------------------------- few rows per kv head ----
-// A tile is NQ x 16 rows; a workgroup of four waves takes one split of the
-// slots, its waves every fourth block of 32.  A wave holds its rows' q and sums
-// in registers; a block's codes come straight from memory into operand
-// registers (no LDS), requested one block ahead.
+// Copy a block to LDS (byte offset `to`, the same in all lanes): every load
+// instruction moves 1 KB, lane l's 16 bytes to `to` + 16 l.
+template <uint32_t BB>
+__device__ __forceinline__ void copy_block(const uint8_t* from, uint32_t to, int lane) {
+  const uint8_t* mine = from + lane * 16;
+#pragma unroll
+  for (uint32_t i = 0; i < BB; i += 1024) {
+    if (BB - i >= 1024 || uint32_t(lane) * 16 < BB - i)
+      asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off nt"
+                   : : "v"(mine + i), "s"(to + i) : "memory", "m0");
+  }
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {   // until at most N loads of the wave are under way
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
 template <int D, int G, int NQ>
-__global__ void __launch_bounds__(256) attend_rows(const AttnParams p) {
-  constexpr int NK = D / 32, NV = D / 16, KG = NK / G, VG = NV / G, NW = 4;
+__global__ void __launch_bounds__(ring_waves(D) * 64, D == 256 ? 1 : 2) attend_rows(const AttnParams p) {
+  typedef Ring<D, G> R;
+  constexpr int NK = D / 32, NV = D / 16, KG = NK / G, VG = NV / G, NW = R::NW, DEPTH = R::DEPTH;
+  constexpr int CK = kchunk(D), CV = vchunk(D);
+  constexpr int LD = D + 4;
+  constexpr uint32_t JOIN = NW * kRowTile * (LD + 2) * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[R::BYTES > JOIN ? R::BYTES : JOIN];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, set = lane >> 4;
-  unsigned id = blockIdx.x;
-  const int split = int(id % unsigned(p.nsplit)); id /= unsigned(p.nsplit);
-  const int tile = int(id % unsigned(p.tiles)); id /= unsigned(p.tiles);
-  const int hk = int(id % unsigned(p.c.heads)), b = int(id / unsigned(p.c.heads));
+  const int split = blockIdx.x, b = blockIdx.z;
+  const int tile = p.tiles == 1 ? 0 : blockIdx.y / unsigned(p.c.heads), hk = blockIdx.y - tile * p.c.heads;
   Span s;
   seq_span(p, b, s);
   const int row0 = tile * NQ * kRowTile;
-  if (row0 >= s.rows) return;
+  if (row0 >= s.rows) {
+    if (p.zero_rest && p.nsplit == 1) zero_rows<D>(p, b, hk, row0, min(row0 + NQ * kRowTile, p.rows));
+    return;
+  }
   tile_span(p, row0, s);
   const int used = used_splits(p, s);
   if (split >= used && split > 0) return;   // split 0 writes the zeros of a tile that sees nothing
@@ -175,7 +202,7 @@ __global__ void __launch_bounds__(256) attend_rows(const AttnParams p) {
   const int nblk = end > begin ? int((end - begin + kBlock - 1) / kBlock) : 0;
   const int mine = nblk > wave ? (nblk - wave + NW - 1) / NW : 0;
 
-  // lane i holds the page of the wave's block i
+  // lane i holds the page of the wave's block i; -1: none
   int page = -1;
   {
     const int64_t slot = begin + int64_t(wave + lane * NW) * kBlock;
@@ -184,17 +211,19 @@ __global__ void __launch_bounds__(256) attend_rows(const AttnParams p) {
     if (page >= p.c.pages) page = -1;
   }
   const int64_t in_page = (int64_t(1) << p.c.shift) - 1;
-  auto where = [&](int i) -> const uint8_t* {
-    const int pg = __builtin_amdgcn_readlane(page, i);
-    if (pg < 0) return nullptr;
+  const uint32_t ring = uint32_t(uintptr_t((__attribute__((address_space(3))) void*)lds)) + uint32_t(wave) * DEPTH * R::BB;
+  // A block without a page is copied from page 0 all the same (the count of
+  // loads under way stays known) and then left out.
+  auto fetch = [&](int i) {
+    const int pg = max(__builtin_amdgcn_readlane(page, i), 0);
     const int64_t slot = begin + int64_t(wave + i * NW) * kBlock;
-    return p.c.buf + uint64_t(pg) * p.c.page_bytes + uint64_t(hk) * p.c.head_bytes +
-           uint32_t((slot & in_page) / kBlock) * block_bytes(D, G);
+    copy_block<R::BB>(p.c.buf + uint64_t(pg) * p.c.page_bytes + uint64_t(hk) * p.c.head_bytes +
+                          uint32_t((slot & in_page) / kBlock) * R::BB,
+                      ring + uint32_t(i % DEPTH) * R::BB, lane);
   };
-
-  BlockRegs<D, G> cur, nxt;
-  const uint8_t* at = mine > 0 ? where(0) : nullptr;
-  if (at) cur.load(at, lane);
+#pragma unroll
+  for (int i = 0; i < DEPTH - 1; i++)
+    if (i < mine) fetch(i);
 
   h8_t qf[NQ][NK];
   float qsum[NQ][G], z_unit[NQ], ref[NQ], top[NQ], psum[NQ], plo[NQ][G];
@@ -237,129 +266,170 @@ __global__ void __launch_bounds__(256) attend_rows(const AttnParams p) {
   // that the largest step seen times 2^lift is near 2^8 (limit 2^15).  Then a
   // product is lost only 2^-33 below the largest, whatever the scale of V.
   float lift = 0.0f, s_limit = -1.0f;
+  float* stash = nullptr;   // z of row n, if it is kept for the weights
+  if (NQ == 1 && p.stash && row0 + n < s.rows)
+    stash = p.stash + ((int64_t(b) * p.c.heads + hk) * p.rows + row0 + n) * p.stash_len;
 
   for (int i = 0; i < mine; i++) {
-    const uint8_t* ahead = i + 1 < mine ? where(i + 1) : nullptr;
-    if (ahead) nxt.load(ahead, lane);
-    if (at) {
-      const int64_t slot0 = begin + int64_t(wave + i * NW) * kBlock;
-      const bool whole = slot0 >= all_from && slot0 + kBlock <= all_to;
-      if (!whole) {   // pairs of slots that hold nothing yet may be anything
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-          if (slot0 + vtoken(set, e) >= s.len)
-#pragma unroll
-            for (int g = 0; g < G; g++) {
-              const uint32_t keep = (e & 1) ? 0x0000ffffu : 0xffff0000u;
-              cur.vs[g][e / 2] &= keep;
-              cur.vl[g][e / 2] &= keep;
-            }
+    if (i + DEPTH - 1 < mine) {
+      fetch(i + DEPTH - 1);
+      wait_loads<R::LOADS * (DEPTH - 1)>();
+    } else {
+      wait_loads<0>();
+    }
+    const int64_t slot0 = begin + int64_t(wave + i * NW) * kBlock;
+    if (__builtin_amdgcn_readlane(page, i) < 0) {
+      if (stash) {
+        const f4_t none = {-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+        *reinterpret_cast<f4_t*>(stash + slot0 + 4 * set) = none;
+        *reinterpret_cast<f4_t*>(stash + slot0 + 16 + 4 * set) = none;
       }
-      float smax = 0.0f;
-      {
-        h2_t m = {(_Float16)0.0f, (_Float16)0.0f};
+      continue;
+    }
+    const uint8_t* blk = lds + (wave * DEPTH + i % DEPTH) * R::BB;
+    const bool whole = slot0 >= all_from && slot0 + kBlock <= all_to;
+    u4_t vs[G], vl[G];
 #pragma unroll
-        for (int g = 0; g < G; g++)
+    for (int g = 0; g < G; g++) {
+      vs[g] = *reinterpret_cast<const u4_t*>(blk + vstep_at(G, set, 0, g));
+      vl[g] = *reinterpret_cast<const u4_t*>(blk + vstep_at(G, set, 0, g) + 16);
+    }
+    if (!whole) {   // pairs of slots that hold nothing yet may be anything
 #pragma unroll
-          for (int e = 0; e < 4; e++) m = __builtin_elementwise_max(m, __builtin_bit_cast(h2_t, (uint32_t)cur.vs[g][e]));
-        smax = fmaxf((float)m[0], (float)m[1]);
-      }
-      float z[NQ][8];
-#pragma unroll
-      for (int u = 0; u < 2; u++) {
-        h8_t kf[NK];
-#pragma unroll
-        for (int ks = 0; ks < NK; ks++) kf[ks] = codes8(cur.k[u][ks / BlockRegs<D, G>::CK][ks % BlockRegs<D, G>::CK]);
-#pragma unroll
-        for (int t = 0; t < NQ; t++) {
-          float zz[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int e = 0; e < 8; e++)
+        if (slot0 + vtoken(set, e) >= s.len)
 #pragma unroll
           for (int g = 0; g < G; g++) {
-            f4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int ks = g * KG; ks < (g + 1) * KG; ks++)
-              a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[ks], qf[t][ks], a, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-              const h2_t pair = __builtin_bit_cast(h2_t, (uint32_t)cur.kp[u][g][r]);
-              zz[r] = fmaf((float)pair[1], a[r], zz[r]);
-              zz[r] = fmaf((float)pair[0], qsum[t][g], zz[r]);
-            }
+            const uint32_t keep = (e & 1) ? 0x0000ffffu : 0xffff0000u;
+            vs[g][e / 2] &= keep;
+            vl[g][e / 2] &= keep;
           }
+    }
+    float smax;
+    {
+      h2_t m = {(_Float16)0.0f, (_Float16)0.0f};
 #pragma unroll
-          for (int r = 0; r < 4; r++) z[t][u * 4 + r] = zz[r] * z_unit[t];
-        }
+      for (int g = 0; g < G; g++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) m = __builtin_elementwise_max(m, __builtin_bit_cast(h2_t, (uint32_t)vs[g][e]));
+      smax = fmaxf((float)m[0], (float)m[1]);
+    }
+    float z[NQ][8];
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      h8_t kf[NK];
+#pragma unroll
+      for (int k = 0; k < NK / CK; k++) {
+        const auto w = *reinterpret_cast<const typename Chunk<CK>::type*>(blk + kcode_at(D, G, u, lane, k * CK));
+#pragma unroll
+        for (int x = 0; x < CK; x++) kf[k * CK + x] = codes8(w[x]);
       }
-      if (!whole) {
+      u4_t kp[G];
 #pragma unroll
-        for (int t = 0; t < NQ; t++)
-#pragma unroll
-          for (int e = 0; e < 8; e++) {
-            const int64_t slot = slot0 + vtoken(set, e);
-            z[t][e] = slot >= from[t] && slot < to[t] ? z[t][e] : -__builtin_inff();
-          }
-      }
-      bool moves = smax > s_limit;
-      float mx[NQ];
+      for (int g = 0; g < G; g++) kp[g] = *reinterpret_cast<const u4_t*>(blk + kpair_at(G, 16 * u + 4 * set, g));
 #pragma unroll
       for (int t = 0; t < NQ; t++) {
-        mx[t] = fmaxf(fmaxf(fmaxf(z[t][0], z[t][1]), fmaxf(z[t][2], z[t][3])),
-                      fmaxf(fmaxf(z[t][4], z[t][5]), fmaxf(z[t][6], z[t][7])));
-        moves |= mx[t] > top[t];
-      }
-      if (__any(moves)) {   // rare: the reference of some row moves
-        float sm = max_sets(smax);
+        float zz[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int d = 1; d < 16; d *= 2) sm = fmaxf(sm, __shfl_xor(sm, d));
-        if (sm > s_limit) {
-          int e = (__builtin_bit_cast(int, fmaxf(sm, 5.9604645e-8f)) >> 23) - 127;   // 2^e <= sm
-          lift = float(8 - e);
-          s_limit = exp2_fast(float(e + 7));
+        for (int g = 0; g < G; g++) {
+          f4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int ks = g * KG; ks < (g + 1) * KG; ks++)
+            a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[ks], qf[t][ks], a, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < 4; r++) {
+            const h2_t pair = __builtin_bit_cast(h2_t, (uint32_t)kp[g][r]);
+            zz[r] = fmaf((float)pair[1], a[r], zz[r]);
+            zz[r] = fmaf((float)pair[0], qsum[t][g], zz[r]);
+          }
         }
 #pragma unroll
-        for (int t = 0; t < NQ; t++) {
-          top[t] = fmaxf(top[t], max_sets(mx[t]));
-          const float r = top[t] - lift, f = exp2_fast(ref[t] - r);
-          ref[t] = r;
-          psum[t] *= f;
-#pragma unroll
-          for (int g = 0; g < G; g++) plo[t][g] *= f;
-#pragma unroll
-          for (int c = 0; c < NV; c++) acc[t][c] *= f;
-        }
+        for (int r = 0; r < 4; r++) z[t][u * 4 + r] = zz[r] * z_unit[t];
       }
-      h8_t pf[NQ][G];
+    }
+    if (!whole) {
 #pragma unroll
       for (int t = 0; t < NQ; t++)
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-          const float pe = exp2_fast(z[t][e] - ref[t]);
-          psum[t] += pe;
-#pragma unroll
-          for (int g = 0; g < G; g++) {
-            const h8_t sv = __builtin_bit_cast(h8_t, cur.vs[g]), lv = __builtin_bit_cast(h8_t, cur.vl[g]);
-            plo[t][g] = fmaf(pe, (float)lv[e], plo[t][g]);
-            pf[t][g][e] = (_Float16)(pe * (float)sv[e]);   // one rounding to 11 bits per product
-          }
+          const int64_t slot = slot0 + vtoken(set, e);
+          z[t][e] = slot >= from[t] && slot < to[t] ? z[t][e] : -__builtin_inff();
         }
+    }
+    if (NQ == 1 && stash) {
+      const f4_t a = {z[0][0], z[0][1], z[0][2], z[0][3]}, c = {z[0][4], z[0][5], z[0][6], z[0][7]};
+      *reinterpret_cast<f4_t*>(stash + slot0 + 4 * set) = a;
+      *reinterpret_cast<f4_t*>(stash + slot0 + 16 + 4 * set) = c;
+    }
+    bool moves = smax > s_limit;
+    float mx[NQ];
 #pragma unroll
-      for (int c = 0; c < NV; c++) {
-        const h8_t vf = codes8(cur.v[c / BlockRegs<D, G>::CV][c % BlockRegs<D, G>::CV]);
+    for (int t = 0; t < NQ; t++) {
+      mx[t] = fmaxf(fmaxf(fmaxf(z[t][0], z[t][1]), fmaxf(z[t][2], z[t][3])),
+                    fmaxf(fmaxf(z[t][4], z[t][5]), fmaxf(z[t][6], z[t][7])));
+      moves |= mx[t] > top[t];
+    }
+    if (__any(moves)) {   // rare: the reference of some row moves
+      float sm = max_sets(smax);
 #pragma unroll
-        for (int t = 0; t < NQ; t++)
-          acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[t][c / VG], acc[t][c], 0, 0, 0);
+      for (int d = 1; d < 16; d *= 2) sm = fmaxf(sm, __shfl_xor(sm, d));
+      if (sm > s_limit) {
+        int e = (__builtin_bit_cast(int, fmaxf(sm, 5.9604645e-8f)) >> 23) - 127;   // 2^e <= sm
+        lift = float(8 - e);
+        s_limit = exp2_fast(float(e + 7));
+      }
+#pragma unroll
+      for (int t = 0; t < NQ; t++) {
+        top[t] = fmaxf(top[t], max_sets(mx[t]));
+        const float r = top[t] - lift, f = exp2_fast(ref[t] - r);
+        ref[t] = r;
+        psum[t] *= f;
+#pragma unroll
+        for (int g = 0; g < G; g++) plo[t][g] *= f;
+#pragma unroll
+        for (int c = 0; c < NV; c++) acc[t][c] *= f;
       }
     }
-    cur = nxt;
-    at = ahead;
+    // p s as the sum of two fp16 (22 bits): one alone costs more than the
+    // rounding of an fp16 result, since the code part is cancelled by p lo.
+    h8_t hi[NQ][G], rest[NQ][G];
+#pragma unroll
+    for (int t = 0; t < NQ; t++)
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const float pe = exp2_fast(z[t][e] - ref[t]);
+        psum[t] += pe;
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+          const h8_t sv = __builtin_bit_cast(h8_t, vs[g]), lv = __builtin_bit_cast(h8_t, vl[g]);
+          plo[t][g] = fmaf(pe, (float)lv[e], plo[t][g]);
+          const float ps = pe * (float)sv[e];
+          hi[t][g][e] = (_Float16)ps;
+          rest[t][g][e] = (_Float16)(ps - (float)hi[t][g][e]);
+        }
+      }
+#pragma unroll
+    for (int k = 0; k < NV / CV; k++) {
+      const auto w = *reinterpret_cast<const typename Chunk<CV>::type*>(blk + vcode_at(D, G, lane, k * CV));
+#pragma unroll
+      for (int x = 0; x < CV; x++) {
+        const int c = k * CV + x;
+        const h8_t vf = codes8(w[x]);
+#pragma unroll
+        for (int t = 0; t < NQ; t++) {
+          acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, hi[t][c / VG], acc[t][c], 0, 0, 0);
+          acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, rest[t][c / VG], acc[t][c], 0, 0, 0);
+        }
+      }
+    }
   }
 
-  // Join the four waves in LDS, in a fixed order.
-  constexpr int LD = D + 4;
-  __shared__ float sums[NW][kRowTile][LD];
-  __shared__ float refs[NW][kRowTile], ls[NW][kRowTile];
+  // Join the waves in LDS, in a fixed order.
+  float* sums = reinterpret_cast<float*>(lds);
+  float* refs = sums + NW * kRowTile * LD;
+  float* ls = refs + NW * kRowTile;
   for (int t = 0; t < NQ; t++) {
-    if (t) __syncthreads();
+    __syncthreads();
     const float l = sum_sets(psum[t]);
     float lo[G];
 #pragma unroll
@@ -369,75 +439,134 @@ __global__ void __launch_bounds__(256) attend_rows(const AttnParams p) {
       f4_t o;
 #pragma unroll
       for (int r = 0; r < 4; r++) o[r] = fmaf(acc[t][c][r], kCodeUnit, lo[c / VG]);
-      *reinterpret_cast<f4_t*>(&sums[wave][n][16 * c + 4 * set]) = o;
+      *reinterpret_cast<f4_t*>(sums + (wave * kRowTile + n) * LD + 16 * c + 4 * set) = o;
     }
-    if (set == 0) { refs[wave][n] = ref[t]; ls[wave][n] = l; }
+    if (set == 0) { refs[wave * kRowTile + n] = ref[t]; ls[wave * kRowTile + n] = l; }
     __syncthreads();
-    for (int it = threadIdx.x; it < kRowTile * (D / 4); it += 256) {
+    for (int it = threadIdx.x; it < kRowTile * (D / 4); it += NW * 64) {
       const int r = it / (D / 4), c = (it % (D / 4)) * 4, row = row0 + t * kRowTile + r;
-      if (row >= s.rows) continue;
-      float m = refs[0][r], l2 = 0.0f;
+      if (row >= s.rows) {
+        if (p.zero_rest && p.nsplit == 1 && row < p.rows)
+          *reinterpret_cast<u2_t*>(out_row(p, b, hk, row) + c) = u2_t{0u, 0u};
+        continue;
+      }
+      float m = refs[r], l2 = 0.0f;
 #pragma unroll
-      for (int w = 1; w < NW; w++) m = fmaxf(m, refs[w][r]);
+      for (int w = 1; w < NW; w++) m = fmaxf(m, refs[w * kRowTile + r]);
       f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int w = 0; w < NW; w++) {
-        const float f = exp2_fast(refs[w][r] - m);
-        l2 = fmaf(ls[w][r], f, l2);
-        const f4_t x = *reinterpret_cast<const f4_t*>(&sums[w][r][c]);
+        const float f = exp2_fast(refs[w * kRowTile + r] - m);
+        l2 = fmaf(ls[w * kRowTile + r], f, l2);
+        const f4_t x = *reinterpret_cast<const f4_t*>(sums + (w * kRowTile + r) * LD + c);
         o += x * f;
       }
+      const int64_t at_row = part_row(p, b, hk, split, row);
       if (p.nsplit == 1) {
-        const float inv = l2 == 0.0f ? 0.0f : 1.0f / l2;
-        u2_t w2;
-        w2[0] = uint32_t(to_16(o[0] * inv, p.q.dtype)) | uint32_t(to_16(o[1] * inv, p.q.dtype)) << 16;
-        w2[1] = uint32_t(to_16(o[2] * inv, p.q.dtype)) | uint32_t(to_16(o[3] * inv, p.q.dtype)) << 16;
-        *reinterpret_cast<u2_t*>(out_row(p, b, hk, row) + c) = w2;
+        put_out(p, b, hk, row, c, o, l2);
         if (p.lse && c == 0) put_lse(p, b, hk, row, m, l2);
       } else if (split < used) {
-        const int64_t at_row = part_row(p, b, hk, split, row);
         *reinterpret_cast<f4_t*>(p.part + at_row * D + c) = o;
-        if (c == 0) { p.part_rl[at_row * 2] = m; p.part_rl[at_row * 2 + 1] = l2; }
       }
+      if (p.part_rl && split < used && c == 0) { p.part_rl[at_row * 2] = m; p.part_rl[at_row * 2 + 1] = l2; }
     }
   }
 }
 
-// Join the splits of a row, in their order: one wave per row.
+// Join the splits of a row, in a fixed order: D / 4 lanes hold the row, and the
+// workgroup's groups of lanes take every NG-th split.
 template <int D>
-__global__ void __launch_bounds__(64) join_kernel(const AttnParams p) {
-  constexpr int PER = D / 32;   // channels per lane of half a wave
-  unsigned id = blockIdx.x;
+__device__ __forceinline__ void join_row(const AttnParams& p, unsigned id, float* lds) {
+  constexpr int LV = D / 4, NG = 256 / LV;
   const int row = int(id % unsigned(p.rows)); id /= unsigned(p.rows);
   const int hk = int(id % unsigned(p.c.heads)), b = int(id / unsigned(p.c.heads));
   Span s;
   seq_span(p, b, s);
-  if (row >= s.rows) return;
+  if (row >= s.rows) {
+    if (p.zero_rest) zero_rows<D>(p, b, hk, row, row + 1);
+    return;
+  }
   tile_span(p, row / p.tile_rows * p.tile_rows, s);
   const int used = used_splits(p, s);
-  const int lane = threadIdx.x, half = lane >> 5, c = (lane & 31) * PER;
+  const int64_t first = part_row(p, b, hk, 0, row);
+  const int lane = threadIdx.x & 63, group = threadIdx.x / LV, c = (threadIdx.x % LV) * 4;
   float m = kNone;
-  for (int i = lane; i < used; i += 64) m = fmaxf(m, p.part_rl[part_row(p, b, hk, i, row) * 2]);
+  for (int i = lane; i < used; i += 64) m = fmaxf(m, p.part_rl[(first + int64_t(i) * p.rows) * 2]);
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
-  float l = 0.0f, o[PER] = {};
-  for (int i = half; i < used; i += 2) {   // even splits in one half of the wave, odd ones in the other
-    const int64_t at = part_row(p, b, hk, i, row);
-    const float f = exp2_fast(p.part_rl[at * 2] - m);
-    l = fmaf(p.part_rl[at * 2 + 1], f, l);
-#pragma unroll
-    for (int k = 0; k < PER; k++) o[k] = fmaf(p.part[at * D + c + k], f, o[k]);
+  float l = 0.0f;
+  f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (group < NG)
+#pragma unroll 4
+    for (int i = group; i < used; i += NG) {
+      const int64_t at = first + int64_t(i) * p.rows;
+      const float f = exp2_fast(p.part_rl[at * 2] - m);
+      l = fmaf(p.part_rl[at * 2 + 1], f, l);
+      o += *reinterpret_cast<const f4_t*>(p.part + at * D + c) * f;
+    }
+  if (group < NG) {
+    *reinterpret_cast<f4_t*>(lds + group * (D + 4) + c) = o;
+    if (c == 0) lds[group * (D + 4) + D] = l;
   }
-  l += __shfl_xor(l, 32);
-#pragma unroll
-  for (int k = 0; k < PER; k++) o[k] += __shfl_xor(o[k], 32);
-  if (half == 0) {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t* dst = out_row(p, b, hk, row) + c;
-#pragma unroll
-    for (int k = 0; k < PER; k++) dst[k] = to_16(o[k] * inv, p.q.dtype);
-    if (p.lse && lane == 0) put_lse(p, b, hk, row, m, l);
+  __syncthreads();
+  if (group == 0) {
+    for (int i = 1; i < NG; i++) {
+      o += *reinterpret_cast<const f4_t*>(lds + i * (D + 4) + c);
+      l += lds[i * (D + 4) + D];
+    }
+    put_out(p, b, hk, row, c, o, l);
+    if (p.lse && c == 0) put_lse(p, b, hk, row, m, l);
   }
+}
+
+// Weights of 1024 slots from the z that attend_rows kept.
+__device__ __forceinline__ void weigh_stash(const AttnParams& p, unsigned id, float* lds) {
+  const unsigned per = unsigned((p.max_len + 1023) / 1024);
+  const int64_t slot = int64_t(id % per) * 1024 + threadIdx.x * 4; id /= per;
+  const int hk = int(id % unsigned(p.c.heads)), b = int(id / unsigned(p.c.heads));
+  Span s;
+  seq_span(p, b, s);
+  if (s.rows == 0) return;
+  tile_span(p, 0, s);
+  const int used = used_splits(p, s);
+  if (slot - threadIdx.x * 4 >= s.hi || used == 0) return;
+  // the rows' log-sum-exp: 32 lanes per row (at most 8 rows)
+  const int r = threadIdx.x >> 5, l32 = threadIdx.x & 31;
+  float m = kNone, l = 0.0f;
+  if (r < s.rows) {
+    const int64_t first = part_row(p, b, hk, 0, r);
+    for (int i = l32; i < used; i += 32) m = fmaxf(m, p.part_rl[(first + int64_t(i) * p.rows) * 2]);
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+    for (int i = l32; i < used; i += 32) {
+      const int64_t at = (first + int64_t(i) * p.rows) * 2;
+      l = fmaf(p.part_rl[at + 1], exp2_fast(p.part_rl[at] - m), l);
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) l += __shfl_xor(l, d);
+    if (l32 == 0) lds[r] = l == 0.0f ? __builtin_inff() : m + __log2f(l);
+  }
+  __syncthreads();
+  if (slot >= s.hi || slot + 4 <= s.lo) return;
+  const float* z = p.stash + (int64_t(b) * p.c.heads + hk) * p.rows * p.stash_len + slot;
+  f4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < s.rows; i++) {
+    const f4_t x = *reinterpret_cast<const f4_t*>(z + i * p.stash_len);
+#pragma unroll
+    for (int k = 0; k < 4; k++) sum[k] += exp2_fast(x[k] - lds[i]);
+  }
+  float* w = p.weights + b * p.wsb + hk * p.wsh + slot;
+#pragma unroll
+  for (int k = 0; k < 4; k++)
+    if (slot + k < s.hi) w[k] += sum[k];
+}
+
+// What follows attend_rows in one launch: rows to join, then slots to weigh.
+template <int D>
+__global__ void __launch_bounds__(256) finish_kernel(const AttnParams p, unsigned joins) {
+  __shared__ float lds[(256 / (D / 4)) * (D + 4)];
+  if (blockIdx.x < joins) join_row<D>(p, blockIdx.x, lds);
+  else weigh_stash(p, blockIdx.x - joins, lds);
 }
 
 // Weight of every cached slot: the sum of P over the sequence's rows, from the
@@ -468,8 +597,7 @@ __global__ void __launch_bounds__(256) weigh_kernel(const AttnParams p) {
       const auto w = *reinterpret_cast<const typename Chunk<CK>::type*>(base + kcode_at(D, G, u, lane, i * CK));
 #pragma unroll
       for (int x = 0; x < CK; x++) {
-        if constexpr (CK == 1) kf[u][i] = codes8(w);
-        else kf[u][i * CK + x] = codes8(w[x]);
+        kf[u][i * CK + x] = codes8(w[x]);
       }
     }
   }
@@ -485,8 +613,8 @@ __global__ void __launch_bounds__(256) weigh_kernel(const AttnParams p) {
     float unit;
     load_q<D>(p, b, hk, row, there, qf, &unit);
     const float z_unit = p.scale2 * kCodeUnit * unit;
-    const int t = row / p.gq;
-    const float l = there ? lse[int64_t(t) * p.q.heads + hk * p.gq + row - t * p.gq] : 0.0f;
+    const int t = token_of(p, row);
+    const float l = there ? lse[int64_t(t) * p.q.heads + (hk - t) * int(p.gq) + row] : 0.0f;
     const float l2 = l * kLog2e;
     float z[8] = {};
 #pragma unroll
@@ -534,8 +662,9 @@ __global__ void __launch_bounds__(256) weigh_kernel(const AttnParams p) {
 // ------------------------------------------------------------- dispatch ----
 struct Plan {
   int nq, tile_rows, tiles, chunk, nsplit;
-  int64_t groups;
-  size_t part, rl, lse, total;   // workspace: floats of the sums, offsets in bytes
+  bool stash;
+  int64_t stash_len, groups, joins, weighs;
+  size_t part, rl, lse, z, total;   // offsets in the workspace, its size
 };
 
 // Variants and splits by shape alone.
@@ -543,32 +672,43 @@ static bool plan(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv
   const int gq = a->q.heads / c->kv_heads;
   const int64_t rows = int64_t(a->q.tokens) * gq;
   if (rows > (int64_t(1) << 30)) return false;
-  pl->nq = rows > kRowTile ? 2 : 1;
+  const int waves = ring_waves(c->head_dim);
+  pl->nq = rows > kRowTile && c->head_dim < 256 ? 2 : 1;
   pl->tile_rows = pl->nq * kRowTile;
   pl->tiles = int((rows + pl->tile_rows - 1) / pl->tile_rows);
-  int64_t span = reach(c, q, a->max_len);
+  const int64_t all = c->pages > 0 ? reach(c, q, a->max_len) : 0;   // without pages there is nothing to see
+  int64_t span = all;
   if (a->window > 0) {   // a tile's rows see at most this many slots, from a block's start
     const int64_t most = int64_t(a->window) + (pl->tile_rows + gq - 1) / gq + 1 + kBlock;
     span = most < span ? most : span;
   }
   const int64_t blocks = (span + kBlock - 1) / kBlock;
-  const int64_t base = int64_t(q->batch) * c->kv_heads * pl->tiles;
-  const int64_t wanted = base > 0 ? (1024 + base - 1) / base : 1;
+  const int64_t heads = int64_t(q->batch) * c->kv_heads;
+  const int64_t base = heads * pl->tiles;
+  const int64_t wanted = base > 0 ? (kWantedGroups + base - 1) / base : 1;
   int64_t per = (blocks + wanted - 1) / wanted;
-  per = per < 8 ? 8 : per > kMaxChunkBlocks ? kMaxChunkBlocks : per;
-  per = (per + 3) / 4 * 4;
+  per = per < kMinBlocks ? kMinBlocks : per > 64 * waves ? 64 * waves : per;   // 64 blocks per wave at most
+  per = (per + waves - 1) / waves * waves;
   pl->chunk = int(per) * kBlock;
   pl->nsplit = int(blocks ? (blocks + per - 1) / per : 1);
   pl->groups = base * pl->nsplit;
-  if (!launchable(pl->groups, 256)) return false;
-  const size_t rows_all = size_t(q->batch) * c->kv_heads * pl->nsplit * size_t(rows);
+  pl->stash = a->weights && rows <= kStashRows;
+  pl->stash_len = (all + kBlock - 1) / kBlock * kBlock;
+  pl->joins = pl->nsplit > 1 ? heads * rows : 0;
+  pl->weighs = !a->weights ? 0 : pl->stash ? heads * ((all + 1023) / 1024) : heads * ((all + 4 * kBlock - 1) / (4 * kBlock));
+  if (q->batch > 65535 || int64_t(pl->tiles) * c->kv_heads > 65535) return false;   // y and z of the grid
+  if (!launchable(pl->groups, 256) || !launchable(pl->joins + pl->weighs, 256)) return false;
+  const size_t rows_all = size_t(heads) * pl->nsplit * size_t(rows);
   size_t o = 0;
-  pl->part = o;
-  if (pl->nsplit > 1) o += (rows_all * c->head_dim * 4 + 255) / 256 * 256;
-  pl->rl = o;
-  if (pl->nsplit > 1) o += (rows_all * 8 + 255) / 256 * 256;
-  pl->lse = o;
-  if (a->weights && !a->lse) o += (size_t(q->batch) * a->q.tokens * a->q.heads * 4 + 255) / 256 * 256;
+  auto take = [&](bool used, size_t bytes) {
+    const size_t at = o;
+    if (used) o += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  pl->part = take(pl->nsplit > 1, rows_all * c->head_dim * 4);
+  pl->rl = take(pl->nsplit > 1 || pl->stash, rows_all * 8);
+  pl->lse = take(a->weights && !pl->stash && !a->lse, size_t(q->batch) * a->q.tokens * a->q.heads * 4);
+  pl->z = take(pl->stash, size_t(heads) * rows * pl->stash_len * 4);
   pl->total = o;
   return true;
 }
@@ -579,21 +719,23 @@ struct LaunchAttention {
   hipStream_t st;
   template <int D, int G>
   int go() {
-    const dim3 grid((unsigned)pl.groups);
-    if (pl.nq == 1) hipLaunchKernelGGL((attend_rows<D, G, 1>), grid, dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((attend_rows<D, G, 2>), grid, dim3(256), 0, st, p);
+    const dim3 grid(unsigned(pl.nsplit), unsigned(pl.tiles * p.c.heads), unsigned(p.c.batch)), threads(Ring<D, G>::NW * 64);
+    if constexpr (D < 256) {
+      if (pl.nq == 2) hipLaunchKernelGGL((attend_rows<D, G, 2>), grid, threads, 0, st, p);
+      else hipLaunchKernelGGL((attend_rows<D, G, 1>), grid, threads, 0, st, p);
+    } else {
+      hipLaunchKernelGGL((attend_rows<D, G, 1>), grid, threads, 0, st, p);
+    }
     int s = launched();
     if (s != STAGQ_OK) return s;
-    if (p.nsplit > 1) {
-      const int64_t n = int64_t(p.c.batch) * p.c.heads * p.rows;
-      hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)n), dim3(64), 0, st, p);
+    const int64_t more = pl.joins + (pl.stash ? pl.weighs : 0);
+    if (more > 0) {
+      hipLaunchKernelGGL((finish_kernel<D>), dim3((unsigned)more), dim3(256), 0, st, p, unsigned(pl.joins));
       s = launched();
       if (s != STAGQ_OK) return s;
     }
-    if (p.weights && p.max_len > 0) {
-      const int64_t per = (p.max_len + 4 * kBlock - 1) / (4 * kBlock);
-      const int64_t n = per * p.c.batch * p.c.heads;
-      hipLaunchKernelGGL((weigh_kernel<D, G>), dim3((unsigned)n), dim3(256), 0, st, p);
+    if (pl.weighs > 0 && !pl.stash) {
+      hipLaunchKernelGGL((weigh_kernel<D, G>), dim3((unsigned)pl.weighs), dim3(256), 0, st, p);
       s = launched();
     }
     return s;
@@ -614,9 +756,6 @@ static int check_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, cons
   if (!(a->scale - a->scale == 0.0f)) return STAGQ_EINVAL;   // infinite or NaN
   if (misaligned(a->q_lens, 4) || misaligned(a->lse, 4) || misaligned(a->weights, 4)) return STAGQ_EALIGN;
   if (a->weights && (a->weights_stride_seq < 0 || a->weights_stride_head < 0)) return STAGQ_EINVAL;
-  const int64_t groups = (reach(c, q, a->max_len) + 4 * kBlock - 1) / (4 * kBlock) * q->batch * c->kv_heads;
-  if (a->weights && !launchable(groups, 256)) return STAGQ_ESHAPE;
-  if (!launchable(int64_t(q->batch) * a->q.tokens * a->q.heads, 64)) return STAGQ_ESHAPE;
   return STAGQ_OK;
 }
 
@@ -649,22 +788,26 @@ int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
   p.q = make_tensor(a->q);
   p.out = make_tensor(a->out);
   p.q_lens = a->q_lens;
-  p.lse = a->lse ? a->lse : a->weights ? reinterpret_cast<float*>(ws + pl.lse) : nullptr;
+  p.lse = a->lse ? a->lse : a->weights && !pl.stash ? reinterpret_cast<float*>(ws + pl.lse) : nullptr;
   p.weights = a->weights;
   p.wsb = a->weights_stride_seq;
   p.wsh = a->weights_stride_head;
   p.part = reinterpret_cast<float*>(ws + pl.part);
-  p.part_rl = reinterpret_cast<float*>(ws + pl.rl);
+  p.part_rl = pl.nsplit > 1 || pl.stash ? reinterpret_cast<float*>(ws + pl.rl) : nullptr;
+  p.stash = pl.stash ? reinterpret_cast<float*>(ws + pl.z) : nullptr;
+  p.stash_len = pl.stash_len;
+  p.zero_rest = a->zero_rest != 0;
   p.scale2 = a->scale * kLog2e;
-  p.gq = a->q.heads / c->kv_heads;
+  p.gq = unsigned(a->q.heads / c->kv_heads);
+  p.gq_inv = p.gq == 1 ? 0xffffffffu : unsigned((uint64_t(1) << 32) / p.gq);
   p.causal = a->causal != 0;
   p.window = a->window;
-  p.max_len = reach(c, q, a->max_len);
+  p.max_len = c->pages > 0 ? reach(c, q, a->max_len) : 0;
   p.chunk = pl.chunk;
   p.nsplit = pl.nsplit;
   p.tiles = pl.tiles;
   p.tile_rows = pl.tile_rows;
-  p.rows = a->q.tokens * p.gq;
+  p.rows = a->q.tokens * int(p.gq);
   return by_shape(c, LaunchAttention{p, pl, static_cast<hipStream_t>(hip_stream)});
 }
 

@@ -66,6 +66,7 @@ struct RowsParams {
   Tensor k, v;
   const int* counts;  // append: new_lens; read: start
   int blocks;         // blocks per sequence in the grid
+  int zero_rest;      // read: rows without a slot are set to 0
 };
 
 // Workgroup -> (block of the sequence's range, head, sequence).
@@ -149,13 +150,15 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const RowsParams p) {
   __shared__ uint8_t vc[kBlock][D];
   int i, head, b;
   place(p, i, head, b);
-  const int64_t start = p.counts ? p.counts[b] : 0;
-  const int64_t end = min(int64_t(p.c.lengths[b]), start + p.k.tokens);
-  const int64_t blk = (start > 0 ? start : 0) / kBlock + i;
-  const int64_t at = blk * kBlock;
-  const int lo = int(max(max(start, int64_t(0)), at) - at), hi = int(max(min(end - at, int64_t(kBlock)), int64_t(0)));
-  if (lo >= hi) return;
-  const uint8_t* base = block_at<D, G>(p.c, b, head, at);   // null: the rows are 0
+  const int64_t start = p.counts ? p.counts[b] : 0, end = start + p.k.tokens;
+  const int64_t at = ((start >> 5) + i) * kBlock;   // block of slots; those below 0 hold nothing
+  const int64_t held = p.c.lengths[b];
+  // rows [lo, hi) of the block are in the tensors, [lo, has) of them in the cache
+  const int lo = int(max(start, at) - at), hi = int(max(min(end - at, int64_t(kBlock)), int64_t(0)));
+  const int has = at < 0 ? 0 : int(max(min(held - at, int64_t(hi)), int64_t(0)));
+  const int last = p.zero_rest ? hi : has;
+  if (lo >= last) return;
+  const uint8_t* base = has > lo ? block_at<D, G>(p.c, b, head, at) : nullptr;   // null: the rows are 0
   if (base) {
     for (int it = threadIdx.x; it < 64 * NV; it += kRowThreads) {
       const int lane = it & 63, ct = it >> 6, set = lane >> 4, c = ct * 16 + (lane & 15);
@@ -166,12 +169,12 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const RowsParams p) {
   }
   __syncthreads();
   const int esz = p.k.dtype == STAGQ_F32 ? 4 : 2;
-  const int items = (hi - lo) * CH;
+  const int items = (last - lo) * CH;
   for (int it = threadIdx.x; it < items; it += kRowThreads) {
     const int tok = lo + it / CH, ch = it % CH;
     const int64_t row = at + tok - start;
     float f[8] = {0, 0, 0, 0, 0, 0, 0, 0}, g[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (base) {
+    if (base && tok < has) {
       const uint32_t w = *reinterpret_cast<const uint32_t*>(
           base + kcode_at(D, G, tok >> 4, (ch & 3) * 16 + (tok & 15), ch >> 2));
       const uint32_t pair = *reinterpret_cast<const uint32_t*>(base + kpair_at(G, tok, ch / LANES));
@@ -254,11 +257,12 @@ int stagq_kv_append(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq
 }
 
 int stagq_kv_read(const stagq_kv_cache* c, const stagq_kv_seqs* q, const int32_t* start, const stagq_kv_tensor* k,
-                  const stagq_kv_tensor* v, void* hip_stream) {
+                  const stagq_kv_tensor* v, int zero_rest, void* hip_stream) {
   RowsParams p;
   const int st = check_rows(c, q, k, v, start, &p);
   if (st != STAGQ_OK) return st;
   if (q->batch == 0 || p.blocks == 0) return STAGQ_OK;
+  p.zero_rest = zero_rest;
   return by_shape(c, LaunchRead{p, static_cast<hipStream_t>(hip_stream)});
 }
 

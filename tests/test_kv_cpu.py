@@ -11,12 +11,66 @@ import pytest
 
 import precision_weight_only_amd as pwo
 from oracle import kv_oracle
-from precision_weight_only_amd import _lib
 
 torch = pytest.importorskip("torch")
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 EINVAL, ESHAPE, EALIGN, ESIZE = -1, -3, -5, -8
+
+
+class KvCache(C.Structure):
+    _fields_ = [
+        ("pages", C.c_int32), ("page_tokens", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
+        ("group", C.c_int32), ("spare", C.c_int32), ("buf", C.c_void_p), ("bytes", C.c_uint64),
+    ]
+
+
+class KvSeqs(C.Structure):
+    _fields_ = [
+        ("batch", C.c_int32), ("table_width", C.c_int32), ("table_stride", C.c_int64), ("table", C.c_void_p),
+        ("lengths", C.c_void_p),
+    ]
+
+
+class KvTensor(C.Structure):
+    _fields_ = [
+        ("data", C.c_void_p), ("dtype", C.c_int32), ("tokens", C.c_int32), ("heads", C.c_int32),
+        ("spare", C.c_int32), ("stride_seq", C.c_int64), ("stride_token", C.c_int64), ("stride_head", C.c_int64),
+    ]
+
+
+class KvAttn(C.Structure):
+    _fields_ = [
+        ("q", KvTensor), ("out", KvTensor), ("q_lens", C.c_void_p), ("lse", C.c_void_p), ("weights", C.c_void_p),
+        ("weights_stride_seq", C.c_int64), ("weights_stride_head", C.c_int64), ("scale", C.c_float),
+        ("causal", C.c_int32), ("window", C.c_int32), ("max_len", C.c_int32), ("zero_rest", C.c_int32),
+        ("spare", C.c_int32),
+    ]
+
+
+class KvEvict(C.Structure):
+    _fields_ = [
+        ("weights", C.c_void_p), ("weights_out", C.c_void_p), ("weights_stride_seq", C.c_int64),
+        ("weights_stride_head", C.c_int64), ("out_stride_seq", C.c_int64), ("out_stride_head", C.c_int64),
+        ("kept", C.c_void_p), ("out_lengths", C.c_void_p), ("out_table", C.c_void_p),
+        ("out_table_stride", C.c_int64), ("out_table_width", C.c_int32), ("keep", C.c_int32), ("sinks", C.c_int32),
+        ("recent", C.c_int32), ("max_len", C.c_int32), ("spare", C.c_int32),
+    ]
+
+
+def test_packed_structs_have_the_layout_of_the_header():
+    from precision_weight_only_amd import kv_cache as m
+    assert m._CACHE.size == C.sizeof(KvCache) and m._SEQS.size == C.sizeof(KvSeqs)
+    assert m._TENSOR.size == C.sizeof(KvTensor) and m._EVICT.size == C.sizeof(KvEvict)
+    assert 2 * m._TENSOR.size + m._ATTN_REST.size == C.sizeof(KvAttn)
+    c = KvCache.from_buffer_copy(m._CACHE.pack(1, 2, 3, 4, 5, 0, 6, 7))
+    assert (c.pages, c.page_tokens, c.kv_heads, c.head_dim, c.group, c.buf, c.bytes) == (1, 2, 3, 4, 5, 6, 7)
+    t = m._TENSOR.pack(1, 2, 3, 4, 0, 5, 6, 7)
+    a = KvAttn.from_buffer_copy(t + t + m._ATTN_REST.pack(1, 2, 3, 4, 5, 0.5, 6, 7, 8, 9, 0))
+    assert (a.out.data, a.out.stride_head, a.q_lens, a.lse, a.weights) == (1, 7, 1, 2, 3)
+    assert (a.weights_stride_head, a.scale, a.causal, a.window, a.max_len, a.zero_rest) == (5, 0.5, 6, 7, 8, 9)
+    e = KvEvict.from_buffer_copy(m._EVICT.pack(*range(1, 17)))
+    assert [getattr(e, f) for f, _ in KvEvict._fields_] == list(range(1, 17))
 
 
 def test_layout_uses_every_byte_once(tmp_path):
@@ -80,27 +134,27 @@ def test_oracle_evict_ties_and_ends():
 def _cache(**kw):
     f = dict(pages=8, page_tokens=64, kv_heads=2, head_dim=128, group=64, spare=0, buf=4096, bytes=1 << 40)
     f.update(kw)
-    return _lib.KvCache(**f)
+    return KvCache(**f)
 
 
 def _seqs(**kw):
     f = dict(batch=3, table_width=4, table_stride=4, table=4096, lengths=4096)
     f.update(kw)
-    return _lib.KvSeqs(**f)
+    return KvSeqs(**f)
 
 
 def _tensor(**kw):
     f = dict(data=4096, dtype=0, tokens=2, heads=2, spare=0, stride_seq=512, stride_token=256, stride_head=128)
     f.update(kw)
-    return _lib.KvTensor(**f)
+    return KvTensor(**f)
 
 
 def _attn(q=None, out=None, **kw):
     q = q or _tensor(heads=4, stride_token=512, stride_seq=1024)
     f = dict(q=q, out=out or q, q_lens=None, lse=None, weights=None, weights_stride_seq=0, weights_stride_head=0,
-             scale=0.1, causal=1, window=0, max_len=0)
+             scale=0.1, causal=1, window=0, max_len=0, zero_rest=0, spare=0)
     f.update(kw)
-    return _lib.KvAttn(**f)
+    return KvAttn(**f)
 
 
 def _evict(**kw):
@@ -108,7 +162,7 @@ def _evict(**kw):
              out_stride_head=256, kept=4096, out_lengths=4096, out_table=4096, out_table_stride=4, out_table_width=4,
              keep=10, sinks=2, recent=3, max_len=0, spare=0)
     f.update(kw)
-    return _lib.KvEvict(**f)
+    return KvEvict(**f)
 
 
 A = C.addressof
@@ -117,7 +171,7 @@ A = C.addressof
 def _rows_calls(c, s, k, v, counts=None):
     lib = pwo.lib()
     return {lib.stagq_kv_append(A(c), A(s), A(k), A(v), counts, None),
-            lib.stagq_kv_read(A(c), A(s), counts, A(k), A(v), None)}
+            lib.stagq_kv_read(A(c), A(s), counts, A(k), A(v), 0, None)}
 
 
 BAD_CACHES = [(dict(page_tokens=48), ESHAPE), (dict(kv_heads=0), ESHAPE), (dict(kv_heads=1025), ESHAPE),

@@ -394,8 +394,8 @@ int stagq_kv_read(const stagq_kv_cache* c, const stagq_kv_seqs* q, const int32_t
  *   max_len  bound of the lengths that sizes the launch (0: the table's width);
  *            a longer sequence is cut to it
  *   zero_rest  not 0: rows of out from q_lens[b] on are set to 0
- * Rows from q_lens[b] on are not read in q, and not written in lse and (without
- * zero_rest) out.  q and out are fp16 or bf16, both the same.
+ * Rows of q from q_lens[b] on do not matter; those of lse and (without zero_rest)
+ * out are left as they were.  q and out are fp16 or bf16, both the same.
  */
 typedef struct {
   stagq_kv_tensor q, out;

@@ -49,7 +49,7 @@ __device__ __forceinline__ int token_of(const AttnParams& p, int row) {
   return int(unsigned(row) - q * p.gq >= p.gq ? q + 1 : q);
 }
 
-// What a sequence and a tile of rows see: slots [lo, hi), lo down to a block.
+// What a sequence and a tile of rows see: slots [lo, hi), lo down to two blocks.
 struct Span {
   int64_t len;
   int ql, rows;     // query tokens and rows of the sequence
@@ -65,7 +65,7 @@ __device__ __forceinline__ void tile_span(const AttnParams& p, int row0, Span& s
   const int last = min(row0 + p.tile_rows, s.rows) - 1;
   const int64_t first_pos = s.len - s.ql + token_of(p, row0), last_pos = s.len - s.ql + token_of(p, last);
   s.hi = p.causal ? max(min(last_pos + 1, s.len), int64_t(0)) : s.len;
-  s.lo = p.window > 0 ? max(first_pos - p.window + 1, int64_t(0)) & ~int64_t(kBlock - 1) : 0;
+  s.lo = p.window > 0 ? max(first_pos - p.window + 1, int64_t(0)) & ~int64_t(2 * kBlock - 1) : 0;
 }
 __device__ __forceinline__ int used_splits(const AttnParams& p, const Span& s) {
   return s.hi <= s.lo ? 0 : int((s.hi - s.lo + p.chunk - 1) / p.chunk);
@@ -108,32 +108,60 @@ __device__ __forceinline__ void zero_rows(const AttnParams& p, int b, int hk, in
     *reinterpret_cast<u2_t*>(out_row(p, b, hk, row + it / (D / 4)) + (it % (D / 4)) * 4) = u2_t{0u, 0u};
 }
 
-// A lane's share of a 16-row query tile as the second operand of the product
-// (row n = lane & 15, channels 32 ks + 8 (lane >> 4) + e), scaled by a power of
-// two per row (see row_scale); *unit undoes it.
+// Query rows as operands.  fp16 rows go in as they are.  bf16 rows are scaled by
+// a power of two per row (see row_scale) and rounded to fp16; the result undoes
+// the scale.  All loads are issued before the first is used.
+template <int N>
+__device__ __forceinline__ float amax_bf16(const u4_t* raw) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; i++)
+#pragma unroll
+    for (int e = 0; e < 8; e++) amax = fmaxf(amax, fabsf(bf16_of(raw[i], e)));
+  return amax;
+}
+template <int N>
+__device__ __forceinline__ void bf16_to_half(const u4_t* raw, float m, h8_t* out) {
+#pragma unroll
+  for (int i = 0; i < N; i++)
+#pragma unroll
+    for (int e = 0; e < 8; e++) out[i][e] = (_Float16)(bf16_of(raw[i], e) * m);
+}
+// Sum of N times eight values as rounded, exact products into binary32.
+template <int N>
+__device__ __forceinline__ float sum8(const h8_t* q) {
+  const h2_t one = {(_Float16)1.0f, (_Float16)1.0f};
+  float a = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    a = __builtin_amdgcn_fdot2(__builtin_shufflevector(q[i], q[i], 0, 1), one, a, false);
+    a = __builtin_amdgcn_fdot2(__builtin_shufflevector(q[i], q[i], 2, 3), one, a, false);
+    a = __builtin_amdgcn_fdot2(__builtin_shufflevector(q[i], q[i], 4, 5), one, a, false);
+    a = __builtin_amdgcn_fdot2(__builtin_shufflevector(q[i], q[i], 6, 7), one, a, false);
+  }
+  return a;
+}
+// A lane's share of a 16-row tile: row n = lane & 15, channels 32 ks + 8 (lane >> 4) + e.
 template <int D>
 __device__ __forceinline__ void load_q(const AttnParams& p, int b, int hk, int row, bool there, h8_t* qf, float* unit) {
+  constexpr int NK = D / 32;
   const int set = (threadIdx.x & 63) >> 4;
-  float f[D / 32][8];
-  float amax = 0.0f;
-  const uint8_t* src = there ? q_row(p, b, hk, row) : nullptr;
+  u4_t raw[NK];
+  const uint8_t* src = q_row(p, b, hk, there ? row : 0);
 #pragma unroll
-  for (int ks = 0; ks < D / 32; ks++) {
-    if (there) {
-      unpack8(src + (32 * ks + 8 * set) * 2, p.q.dtype, f[ks]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; e++) f[ks][e] = 0.0f;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; e++) amax = fmaxf(amax, fabsf(f[ks][e]));
+  for (int ks = 0; ks < NK; ks++) {
+    raw[ks] = u4_t{0u, 0u, 0u, 0u};
+    if (there) raw[ks] = *reinterpret_cast<const u4_t*>(src + (32 * ks + 8 * set) * 2);
   }
-  const float m = row_scale(max_sets(amax));
-  *unit = 1.0f / m;
+  *unit = 1.0f;
+  if (p.q.dtype == STAGQ_F16) {
 #pragma unroll
-  for (int ks = 0; ks < D / 32; ks++)
-#pragma unroll
-    for (int e = 0; e < 8; e++) qf[ks][e] = (_Float16)(f[ks][e] * m);
+    for (int ks = 0; ks < NK; ks++) qf[ks] = __builtin_bit_cast(h8_t, raw[ks]);
+  } else {
+    const float m = row_scale(max_sets(amax_bf16<NK>(raw)));
+    bf16_to_half<NK>(raw, m, qf);
+    *unit = 1.0f / m;
+  }
 }
 
 template <int N>
@@ -141,6 +169,62 @@ struct Chunk;
 template <> struct Chunk<2> { typedef u2_t type; };
 template <> struct Chunk<3> { struct type { uint32_t v[3]; __device__ uint32_t operator[](int i) const { return v[i]; } }; };
 template <> struct Chunk<4> { typedef u4_t type; };
+
+// The waves' sums of a tile of ROWS rows meet in LDS: [wave][row][D + 4] floats,
+// then the references and sums of p, [wave][row] each.
+constexpr uint32_t join_bytes(int waves, int rows, int D) { return uint32_t(waves * rows * (D + 4 + 2) * 4); }
+__device__ __forceinline__ void join_refs(float* sums, int waves, int rows, int D, int wave, int row, float ref, float l) {
+  float* refs = sums + waves * rows * (D + 4);
+  refs[wave * rows + row] = ref;
+  refs[(waves + wave) * rows + row] = l;
+}
+// Add them up in a fixed order and write the rows from row0 on: the result
+// where the slots are not split, else the split's part.
+template <int D, int NW, int ROWS>
+__device__ __forceinline__ void join_waves(const AttnParams& p, const Span& s, const float* sums, int b, int hk, int split,
+                                           int used, int row0) {
+  constexpr int LD = D + 4;
+  const float* refs = sums + NW * ROWS * LD;
+  const float* ls = refs + NW * ROWS;
+  for (int it = threadIdx.x; it < ROWS * (D / 4); it += NW * 64) {
+    const int r = it / (D / 4), c = (it % (D / 4)) * 4, row = row0 + r;
+    if (row >= s.rows) {
+      if (p.zero_rest && p.nsplit == 1 && row < p.rows)
+        *reinterpret_cast<u2_t*>(out_row(p, b, hk, row) + c) = u2_t{0u, 0u};
+      continue;
+    }
+    float m = refs[r], l = 0.0f;
+#pragma unroll
+    for (int w = 1; w < NW; w++) m = fmaxf(m, refs[w * ROWS + r]);
+    f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < NW; w++) {
+      const float f = exp2_fast(refs[w * ROWS + r] - m);
+      l = fmaf(ls[w * ROWS + r], f, l);
+      o += *reinterpret_cast<const f4_t*>(sums + (w * ROWS + r) * LD + c) * f;
+    }
+    const int64_t at = part_row(p, b, hk, split, row);
+    if (p.nsplit == 1) {
+      put_out(p, b, hk, row, c, o, l);
+      if (p.lse && c == 0) put_lse(p, b, hk, row, m, l);
+    } else if (split < used) {
+      *reinterpret_cast<f4_t*>(p.part + at * D + c) = o;
+    }
+    if (p.part_rl && split < used && c == 0) { p.part_rl[at * 2] = m; p.part_rl[at * 2 + 1] = l; }
+  }
+}
+
+// p s goes into fp16: the reference lies `lift` below the row's largest z, so
+// that the largest step seen times 2^lift is near 2^8 (limit 2^15).  Then a
+// product is lost only 2^-33 below the largest, whatever the scale of V.  smax:
+// largest step of what comes next, the same in all lanes.
+__device__ __forceinline__ void lift_of(float smax, float& lift, float& s_limit) {
+  if (smax > s_limit) {
+    const int e = (__builtin_bit_cast(int, fmaxf(smax, 5.9604645e-8f)) >> 23) - 127;   // 2^e <= smax
+    lift = float(8 - e);
+    s_limit = exp2_fast(float(e + 7));
+  }
+}
 
 // ------------------------------------------------- few rows per kv head ----
 // A tile is NQ x 16 rows; a workgroup takes one split of the slots, its waves
@@ -182,7 +266,7 @@ __global__ void __launch_bounds__(ring_waves(D) * 64, D == 256 ? 1 : 2) attend_r
   constexpr int NK = D / 32, NV = D / 16, KG = NK / G, VG = NV / G, NW = R::NW, DEPTH = R::DEPTH;
   constexpr int CK = kchunk(D), CV = vchunk(D);
   constexpr int LD = D + 4;
-  constexpr uint32_t JOIN = NW * kRowTile * (LD + 2) * 4;
+  constexpr uint32_t JOIN = join_bytes(NW, kRowTile, D);
   __shared__ __attribute__((aligned(16))) uint8_t lds[R::BYTES > JOIN ? R::BYTES : JOIN];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, set = lane >> 4;
@@ -238,12 +322,7 @@ __global__ void __launch_bounds__(ring_waves(D) * 64, D == 256 ? 1 : 2) attend_r
     z_unit[t] = p.scale2 * kCodeUnit * unit;
 #pragma unroll
     for (int g = 0; g < G; g++) {
-      float a = 0.0f;
-#pragma unroll
-      for (int ks = g * KG; ks < (g + 1) * KG; ks++)
-#pragma unroll
-        for (int e = 0; e < 8; e++) a += (float)qf[t][ks][e];
-      qsum[t][g] = sum_sets(a) * (1.0f / kCodeUnit);
+      qsum[t][g] = sum_sets(sum8<KG>(qf[t] + g * KG)) * (1.0f / kCodeUnit);
       plo[t][g] = 0.0f;
     }
     from[t] = to[t] = 0;
@@ -262,14 +341,12 @@ __global__ void __launch_bounds__(ring_waves(D) * 64, D == 256 ? 1 : 2) attend_r
     row_span(p, s, min(row0 + NQ * kRowTile, s.rows) - 1, f, t);
     all_from = f;
   }
-  // p s goes into fp16: the reference lies `lift` below the row's largest z, so
-  // that the largest step seen times 2^lift is near 2^8 (limit 2^15).  Then a
-  // product is lost only 2^-33 below the largest, whatever the scale of V.
   float lift = 0.0f, s_limit = -1.0f;
   float* stash = nullptr;   // z of row n, if it is kept for the weights
   if (NQ == 1 && p.stash && row0 + n < s.rows)
     stash = p.stash + ((int64_t(b) * p.c.heads + hk) * p.rows + row0 + n) * p.stash_len;
 
+#pragma unroll 1
   for (int i = 0; i < mine; i++) {
     if (i + DEPTH - 1 < mine) {
       fetch(i + DEPTH - 1);
@@ -373,11 +450,7 @@ __global__ void __launch_bounds__(ring_waves(D) * 64, D == 256 ? 1 : 2) attend_r
       float sm = max_sets(smax);
 #pragma unroll
       for (int d = 1; d < 16; d *= 2) sm = fmaxf(sm, __shfl_xor(sm, d));
-      if (sm > s_limit) {
-        int e = (__builtin_bit_cast(int, fmaxf(sm, 5.9604645e-8f)) >> 23) - 127;   // 2^e <= sm
-        lift = float(8 - e);
-        s_limit = exp2_fast(float(e + 7));
-      }
+      lift_of(sm, lift, s_limit);
 #pragma unroll
       for (int t = 0; t < NQ; t++) {
         top[t] = fmaxf(top[t], max_sets(mx[t]));
@@ -424,10 +497,7 @@ __global__ void __launch_bounds__(ring_waves(D) * 64, D == 256 ? 1 : 2) attend_r
     }
   }
 
-  // Join the waves in LDS, in a fixed order.
   float* sums = reinterpret_cast<float*>(lds);
-  float* refs = sums + NW * kRowTile * LD;
-  float* ls = refs + NW * kRowTile;
   for (int t = 0; t < NQ; t++) {
     __syncthreads();
     const float l = sum_sets(psum[t]);
@@ -441,36 +511,256 @@ __global__ void __launch_bounds__(ring_waves(D) * 64, D == 256 ? 1 : 2) attend_r
       for (int r = 0; r < 4; r++) o[r] = fmaf(acc[t][c][r], kCodeUnit, lo[c / VG]);
       *reinterpret_cast<f4_t*>(sums + (wave * kRowTile + n) * LD + 16 * c + 4 * set) = o;
     }
-    if (set == 0) { refs[wave * kRowTile + n] = ref[t]; ls[wave * kRowTile + n] = l; }
+    if (set == 0) join_refs(sums, NW, kRowTile, D, wave, n, ref[t], l);
     __syncthreads();
-    for (int it = threadIdx.x; it < kRowTile * (D / 4); it += NW * 64) {
-      const int r = it / (D / 4), c = (it % (D / 4)) * 4, row = row0 + t * kRowTile + r;
-      if (row >= s.rows) {
-        if (p.zero_rest && p.nsplit == 1 && row < p.rows)
-          *reinterpret_cast<u2_t*>(out_row(p, b, hk, row) + c) = u2_t{0u, 0u};
-        continue;
-      }
-      float m = refs[r], l2 = 0.0f;
-#pragma unroll
-      for (int w = 1; w < NW; w++) m = fmaxf(m, refs[w * kRowTile + r]);
-      f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int w = 0; w < NW; w++) {
-        const float f = exp2_fast(refs[w * kRowTile + r] - m);
-        l2 = fmaf(ls[w * kRowTile + r], f, l2);
-        const f4_t x = *reinterpret_cast<const f4_t*>(sums + (w * kRowTile + r) * LD + c);
-        o += x * f;
-      }
-      const int64_t at_row = part_row(p, b, hk, split, row);
-      if (p.nsplit == 1) {
-        put_out(p, b, hk, row, c, o, l2);
-        if (p.lse && c == 0) put_lse(p, b, hk, row, m, l2);
-      } else if (split < used) {
-        *reinterpret_cast<f4_t*>(p.part + at_row * D + c) = o;
-      }
-      if (p.part_rl && split < used && c == 0) { p.part_rl[at_row * 2] = m; p.part_rl[at_row * 2 + 1] = l2; }
-    }
+    join_waves<D, NW, kRowTile>(p, s, sums, b, hk, split, used, row0 + t * kRowTile);
   }
+}
+
+// ------------------------------------------ up to four rows per kv head ----
+// The decode step of most models: one token, at most four q heads per kv head.
+// In attend_rows twelve of the sixteen columns would idle and its vector work
+// (58 % of the cycles at 131001 slots; matrix 12 %) would bound it.  Here the
+// matrix instruction is the one of sixteen 4 x 4 x 4 products: four rows against
+// 64 slots (lane = slot for K, then four slots of row lane & 3 per lane), and
+// for V the product of one set of four slots, its probabilities broadcast from
+// the four lanes that hold them, with 64 channels (lane = channel).  Per 64
+// slots that is a quarter of the vector work outside the unpacking of codes,
+// at the same matrix cycles.
+// Waves, rings and the running reference as in attend_rows; a step is two
+// blocks, and the next step's are under way.
+constexpr int few_waves(int D) { return D == 256 ? 2 : 4; }
+constexpr int kFewRows = 4;
+constexpr int kFewDepth = 4;   // blocks of a ring
+
+template <int D, int G>
+__global__ void __launch_bounds__(few_waves(D) * 64, D == 256 ? 1 : 2) attend_few(const AttnParams p) {
+  constexpr int NW = few_waves(D), NK = D / 32, NH = D / 64, KG = NK / G, CK = kchunk(D), LD = D + 4;
+  constexpr uint32_t BB = block_bytes(D, G);
+  constexpr int LOADS = 2 * int((BB + 1023) / 1024);   // of a wave per step
+  constexpr uint32_t RING = NW * kFewDepth * BB, JOIN = join_bytes(NW, kFewRows, D);
+  __shared__ __attribute__((aligned(16))) uint8_t lds[RING > JOIN ? RING : JOIN];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int j = lane & 3, quad = lane >> 2;   // row, and set of four slots of the step
+  const int split = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
+  // the row, and (bf16) a lane's part of it for its largest magnitude: requested
+  // before anything that depends on the lengths
+  constexpr int PART = (D / 8 + 15) / 16;
+  u4_t raw[D / 8], part[PART];
+  {
+    const u4_t* src = reinterpret_cast<const u4_t*>(q_row(p, b, hk, min(j, p.rows - 1)));
+#pragma unroll
+    for (int c = 0; c < D / 8; c++) raw[c] = src[c];
+#pragma unroll
+    for (int c = 0; c < PART; c++) part[c] = src[(c * 16 + quad) % (D / 8)];
+  }
+  Span s;
+  seq_span(p, b, s);
+  if (s.rows == 0) {
+    if (p.zero_rest && p.nsplit == 1) zero_rows<D>(p, b, hk, 0, p.rows);
+    return;
+  }
+  tile_span(p, 0, s);
+  const int used = used_splits(p, s);
+  if (split >= used && split > 0) return;   // split 0 writes the zeros of rows that see nothing
+  const int64_t begin = s.lo + int64_t(split) * p.chunk, end = min(begin + p.chunk, s.hi);
+  const int nstep = end > begin ? int((end - begin + 2 * kBlock - 1) / (2 * kBlock)) : 0;
+  const int mine = nstep > wave ? (nstep - wave + NW - 1) / NW : 0;
+
+  // lane i holds the page of the wave's block i (two per step); -1: none
+  int page = -1;
+  {
+    const int64_t slot = begin + int64_t((wave + (lane >> 1) * NW) * 2 + (lane & 1)) * kBlock;
+    const int64_t e = slot >> p.c.shift;
+    if ((lane >> 1) < mine && slot < end && e < p.c.width) page = p.c.table[int64_t(b) * p.c.table_stride + e];
+    if (page >= p.c.pages) page = -1;
+  }
+  const int64_t in_page = (int64_t(1) << p.c.shift) - 1;
+  const uint32_t ring = uint32_t(uintptr_t((__attribute__((address_space(3))) void*)lds)) + uint32_t(wave) * kFewDepth * BB;
+  auto fetch = [&](int i) {   // a block without a page is copied from page 0 and left out
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const int pg = max(__builtin_amdgcn_readlane(page, 2 * i + h), 0);
+      const int64_t slot = begin + int64_t((wave + i * NW) * 2 + h) * kBlock;
+      copy_block<BB>(p.c.buf + uint64_t(pg) * p.c.page_bytes + uint64_t(hk) * p.c.head_bytes +
+                         uint32_t((slot & in_page) / kBlock) * BB,
+                     ring + uint32_t((2 * i + h) % kFewDepth) * BB, lane);
+    }
+  };
+  if (mine > 0) fetch(0);
+
+  // q of row j, all channels (lanes of one row hold the same)
+  h8_t qf[D / 8];
+  float qsum[G], z_unit = p.scale2 * kCodeUnit;
+  const bool there = j < s.rows;
+  if (p.q.dtype == STAGQ_F16) {
+#pragma unroll
+    for (int c = 0; c < D / 8; c++) qf[c] = __builtin_bit_cast(h8_t, raw[c]);
+  } else {
+    const float m = row_scale(max_quads(amax_bf16<PART>(part)));
+    bf16_to_half<D / 8>(raw, m, qf);
+    z_unit /= m;
+  }
+#pragma unroll
+  for (int g = 0; g < G; g++) qsum[g] = sum8<D / 8 / G>(qf + g * (D / 8 / G)) * (1.0f / kCodeUnit);
+  int64_t from = 0, to = 0;
+  if (there) row_span(p, s, j, from, to);
+  int64_t all_from, all_to;   // slots that every row sees
+  {
+    int64_t f, t;
+    row_span(p, s, 0, f, all_to);
+    row_span(p, s, s.rows - 1, all_from, t);
+  }
+  float* stash = nullptr;
+  if (p.stash && there) stash = p.stash + ((int64_t(b) * p.c.heads + hk) * p.rows + j) * p.stash_len;
+
+  float ref = kNone, top = kNone, psum = 0.0f, plo[G], lift = 0.0f, s_limit = -1.0f;
+  f4_t acc[NH], more[NH];   // of the two parts of p s
+#pragma unroll
+  for (int g = 0; g < G; g++) plo[g] = 0.0f;
+#pragma unroll
+  for (int h = 0; h < NH; h++) acc[h] = more[h] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+#pragma unroll 1
+  for (int i = 0; i < mine; i++) {
+    if (i + 1 < mine) {
+      fetch(i + 1);
+      wait_loads<LOADS>();
+    } else {
+      wait_loads<0>();
+    }
+    const int64_t slot0 = begin + int64_t(wave + i * NW) * 2 * kBlock;
+    const uint8_t* step = lds + (wave * kFewDepth + (2 * i) % kFewDepth) * BB;   // its two blocks are neighbours
+    const bool gone0 = __builtin_amdgcn_readlane(page, 2 * i) < 0, gone1 = __builtin_amdgcn_readlane(page, 2 * i + 1) < 0;
+    const bool whole = slot0 >= all_from && slot0 + 2 * kBlock <= all_to && !gone0 && !gone1;
+    // scores: lane = slot for the codes, then slots 4 quad .. 4 quad + 3 of row j
+    f4_t a[G][2];
+#pragma unroll
+    for (int g = 0; g < G; g++) a[g][0] = a[g][1] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    {
+      const uint8_t* kb = step + (lane >> 5) * BB;
+      const int u = (lane >> 4) & 1, t = lane & 15;
+#pragma unroll
+      for (int c = 0; c < 4; c++)
+#pragma unroll
+        for (int k = 0; k < NK / CK; k++) {
+          const auto w = *reinterpret_cast<const typename Chunk<CK>::type*>(kb + kcode_at(D, G, u, c * 16 + t, k * CK));
+#pragma unroll
+          for (int x = 0; x < CK; x++) {
+            const int ks = k * CK + x;
+            const h8_t f = codes8(w[x]);
+            const h8_t q = qf[ks * 4 + c];
+            a[ks / KG][0] = __builtin_amdgcn_mfma_f32_4x4x4f16(low4(f), low4(q), a[ks / KG][0], 0, 0, 0);
+            a[ks / KG][1] = __builtin_amdgcn_mfma_f32_4x4x4f16(high4(f), high4(q), a[ks / KG][1], 0, 0, 0);
+          }
+        }
+    }
+    const uint8_t* mb = step + (quad >> 3) * BB;   // the block of the lane's four slots
+    const int q8 = quad & 7;
+    float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    h4_t vs[G], vl[G];
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+      const u4_t kp = *reinterpret_cast<const u4_t*>(mb + kpair_at(G, 4 * q8, g));
+      vs[g] = *reinterpret_cast<const h4_t*>(mb + vstep_at(G, q8 & 3, 4 * (q8 >> 2), g));
+      vl[g] = *reinterpret_cast<const h4_t*>(mb + vstep_at(G, q8 & 3, 4 * (q8 >> 2), g) + 16);
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const h2_t pair = __builtin_bit_cast(h2_t, (uint32_t)kp[r]);
+        z[r] = fmaf((float)pair[1], a[g][0][r] + a[g][1][r], z[r]);
+        z[r] = fmaf((float)pair[0], qsum[g], z[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; r++) z[r] *= z_unit;
+    if (!whole) {
+      const bool gone = quad < 8 ? gone0 : gone1;
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const int64_t slot = slot0 + 4 * quad + r;
+        z[r] = slot >= from && slot < to && !gone ? z[r] : -__builtin_inff();
+        if (slot >= s.len || gone)   // pairs of slots that hold nothing may be anything
+#pragma unroll
+          for (int g = 0; g < G; g++) vs[g][r] = vl[g][r] = (_Float16)0.0f;
+      }
+    }
+    if (stash && slot0 + 4 * quad < p.stash_len) *reinterpret_cast<f4_t*>(stash + slot0 + 4 * quad) = f4_t{z[0], z[1], z[2], z[3]};
+    h2_t sm2 = {(_Float16)0.0f, (_Float16)0.0f};
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+      sm2 = __builtin_elementwise_max(sm2, __builtin_shufflevector(vs[g], vs[g], 0, 1));
+      sm2 = __builtin_elementwise_max(sm2, __builtin_shufflevector(vs[g], vs[g], 2, 3));
+    }
+    const float smax = fmaxf((float)sm2[0], (float)sm2[1]);
+    const float mx = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+    if (__any(smax > s_limit || mx > top)) {   // rare: the reference of some row moves
+      float sm = max_quads(smax);
+      sm = fmaxf(sm, __shfl_xor(sm, 1));
+      sm = fmaxf(sm, __shfl_xor(sm, 2));
+      lift_of(sm, lift, s_limit);
+      top = fmaxf(top, max_quads(mx));
+      const float r = top - lift, f = exp2_fast(ref - r);
+      ref = r;
+      psum *= f;
+#pragma unroll
+      for (int g = 0; g < G; g++) plo[g] *= f;
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const float fq = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), q));
+#pragma unroll
+        for (int h = 0; h < NH; h++) {
+          acc[h][q] *= fq;
+          more[h][q] *= fq;
+        }
+      }
+    }
+    h4_t hi[G], rest[G];   // p s as the sum of two fp16, see attend_rows
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+      const float pe = exp2_fast(z[r] - ref);
+      psum += pe;
+#pragma unroll
+      for (int g = 0; g < G; g++) {
+        plo[g] = fmaf(pe, (float)vl[g][r], plo[g]);
+        const float ps = pe * (float)vs[g][r];
+        hi[g][r] = (_Float16)ps;
+        rest[g][r] = (_Float16)(ps - (float)hi[g][r]);
+      }
+    }
+    // V: lane = channel 64 h + lane; a dword holds two sets of four slots
+#define STAGQ_KV_PV(HB, C)                                                                                        \
+  {                                                                                                               \
+    _Pragma("unroll") for (int h = 0; h < NH; h++) {                                                              \
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(step + HB * BB +                                      \
+                                                            vcode_at(D, G, C * 16 + (lane & 15), 4 * h + (lane >> 4))); \
+      const h8_t f = codes8(w);                                                                                   \
+      const int g = h * G / NH;                                                                                   \
+      acc[h] = __builtin_amdgcn_mfma_f32_4x4x4f16(hi[g], low4(f), acc[h], 4, 8 * HB + C, 0);                           \
+      more[h] = __builtin_amdgcn_mfma_f32_4x4x4f16(rest[g], low4(f), more[h], 4, 8 * HB + C, 0);                       \
+      acc[h] = __builtin_amdgcn_mfma_f32_4x4x4f16(hi[g], high4(f), acc[h], 4, 8 * HB + 4 + C, 0);                       \
+      more[h] = __builtin_amdgcn_mfma_f32_4x4x4f16(rest[g], high4(f), more[h], 4, 8 * HB + 4 + C, 0);                   \
+    }                                                                                                             \
+  }
+    STAGQ_KV_PV(0, 0) STAGQ_KV_PV(0, 1) STAGQ_KV_PV(0, 2) STAGQ_KV_PV(0, 3)
+    STAGQ_KV_PV(1, 0) STAGQ_KV_PV(1, 1) STAGQ_KV_PV(1, 2) STAGQ_KV_PV(1, 3)
+#undef STAGQ_KV_PV
+  }
+
+  float* sums = reinterpret_cast<float*>(lds);
+  __syncthreads();
+  const float l = sum_quads(psum);
+#pragma unroll
+  for (int g = 0; g < G; g++) plo[g] = sum_quads(plo[g]);
+#pragma unroll
+  for (int h = 0; h < NH; h++)
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      const float lo = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, plo[h * G / NH]), q));
+      sums[(wave * kFewRows + q) * LD + 64 * h + lane] = fmaf(acc[h][q] + more[h][q], kCodeUnit, lo);
+    }
+  if (quad == 0) join_refs(sums, NW, kFewRows, D, wave, j, ref, l);
+  __syncthreads();
+  join_waves<D, NW, kFewRows>(p, s, sums, b, hk, split, used, 0);
 }
 
 // Join the splits of a row, in a fixed order: D / 4 lanes hold the row, and the
@@ -619,12 +909,7 @@ __global__ void __launch_bounds__(256) weigh_kernel(const AttnParams p) {
     float z[8] = {};
 #pragma unroll
     for (int g = 0; g < G; g++) {
-      float qs = 0.0f;
-#pragma unroll
-      for (int ks = g * KG; ks < (g + 1) * KG; ks++)
-#pragma unroll
-        for (int e = 0; e < 8; e++) qs += (float)qf[ks][e];
-      qs = sum_sets(qs) * (1.0f / kCodeUnit);
+      const float qs = sum_sets(sum8<KG>(qf + g * KG)) * (1.0f / kCodeUnit);
 #pragma unroll
       for (int u = 0; u < 2; u++) {
         f4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -661,7 +946,7 @@ __global__ void __launch_bounds__(256) weigh_kernel(const AttnParams p) {
 
 // ------------------------------------------------------------- dispatch ----
 struct Plan {
-  int nq, tile_rows, tiles, chunk, nsplit;
+  int nq, tile_rows, tiles, chunk, nsplit;   // nq 0: attend_few
   bool stash;
   int64_t stash_len, groups, joins, weighs;
   size_t part, rl, lse, z, total;   // offsets in the workspace, its size
@@ -673,13 +958,14 @@ static bool plan(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv
   const int64_t rows = int64_t(a->q.tokens) * gq;
   if (rows > (int64_t(1) << 30)) return false;
   const int waves = ring_waves(c->head_dim);
-  pl->nq = rows > kRowTile && c->head_dim < 256 ? 2 : 1;
-  pl->tile_rows = pl->nq * kRowTile;
+  const bool few = rows <= kFewRows && c->group >= 64;   // a set of 64 channels shares its pair there
+  pl->nq = few ? 0 : rows > kRowTile && c->head_dim < 256 ? 2 : 1;
+  pl->tile_rows = few ? kFewRows : pl->nq * kRowTile;
   pl->tiles = int((rows + pl->tile_rows - 1) / pl->tile_rows);
   const int64_t all = c->pages > 0 ? reach(c, q, a->max_len) : 0;   // without pages there is nothing to see
   int64_t span = all;
-  if (a->window > 0) {   // a tile's rows see at most this many slots, from a block's start
-    const int64_t most = int64_t(a->window) + (pl->tile_rows + gq - 1) / gq + 1 + kBlock;
+  if (a->window > 0) {   // a tile's rows see at most this many slots, from the start of two blocks
+    const int64_t most = int64_t(a->window) + (pl->tile_rows + gq - 1) / gq + 1 + 2 * kBlock;
     span = most < span ? most : span;
   }
   const int64_t blocks = (span + kBlock - 1) / kBlock;
@@ -688,7 +974,7 @@ static bool plan(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv
   const int64_t wanted = base > 0 ? (kWantedGroups + base - 1) / base : 1;
   int64_t per = (blocks + wanted - 1) / wanted;
   per = per < kMinBlocks ? kMinBlocks : per > 64 * waves ? 64 * waves : per;   // 64 blocks per wave at most
-  per = (per + waves - 1) / waves * waves;
+  per = (per + 2 * waves - 1) / (2 * waves) * (2 * waves);
   pl->chunk = int(per) * kBlock;
   pl->nsplit = int(blocks ? (blocks + per - 1) / per : 1);
   pl->groups = base * pl->nsplit;
@@ -720,7 +1006,11 @@ struct LaunchAttention {
   template <int D, int G>
   int go() {
     const dim3 grid(unsigned(pl.nsplit), unsigned(pl.tiles * p.c.heads), unsigned(p.c.batch)), threads(Ring<D, G>::NW * 64);
-    if constexpr (D < 256) {
+    if constexpr (D / G >= 64) {
+      if (pl.nq == 0) hipLaunchKernelGGL((attend_few<D, G>), grid, dim3(few_waves(D) * 64), 0, st, p);
+    }
+    if (pl.nq == 0) {
+    } else if constexpr (D < 256) {
       if (pl.nq == 2) hipLaunchKernelGGL((attend_rows<D, G, 2>), grid, threads, 0, st, p);
       else hipLaunchKernelGGL((attend_rows<D, G, 1>), grid, threads, 0, st, p);
     } else {

@@ -90,6 +90,18 @@ __device__ __forceinline__ float sum_sets(float v) {
   return v + __shfl_xor(v, 32);
 }
 
+// Reductions over the sixteen lanes of one residue modulo 4.
+__device__ __forceinline__ float max_quads(float v) {
+#pragma unroll
+  for (int d = 4; d < 64; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+__device__ __forceinline__ float sum_quads(float v) {
+#pragma unroll
+  for (int d = 4; d < 64; d *= 2) v += __shfl_xor(v, d);
+  return v;
+}
+
 __device__ __forceinline__ void unpack8(const uint8_t* p, int dtype, float* f) {
   if (dtype == STAGQ_F32) {
     const f4_t a = *reinterpret_cast<const f4_t*>(p), b = *reinterpret_cast<const f4_t*>(p + 16);
@@ -107,15 +119,22 @@ __device__ __forceinline__ void unpack8(const uint8_t* p, int dtype, float* f) {
     }
   }
 }
+// Element e of eight bf16 values.
+__device__ __forceinline__ float bf16_of(u4_t v, int e) {
+  const uint32_t w = v[e / 2];
+  return __builtin_bit_cast(float, (e & 1) ? w & 0xffff0000u : w << 16);
+}
+__device__ __forceinline__ h4_t low4(h8_t v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3); }
+__device__ __forceinline__ h4_t high4(h8_t v) { return __builtin_shufflevector(v, v, 4, 5, 6, 7); }
 __device__ __forceinline__ uint16_t to_16(float v, int dtype) {  // one rounding, nearest even
   if (dtype == STAGQ_F16) return __builtin_bit_cast(uint16_t, (_Float16)v);
   return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// 2^e with e chosen so that the largest magnitude of a query row lands in
-// [2^14, 2^15): the row times 2^e in fp16 is exact for fp16 and bf16 rows but
-// for elements some 2^24 below the largest.  Returns the factor (1 for a row of
-// zeros); a row with an infinity or NaN gets 1 and keeps them.
+// 2^e with e chosen so that the largest magnitude of a bf16 row lands in
+// [2^14, 2^15): the row times 2^e in fp16 is exact but for elements some 2^24
+// below the largest.  1 for a row of zeros and one with an infinity or NaN
+// (which stay what they are).
 __device__ __forceinline__ float row_scale(float amax) {
   const uint32_t e = (__builtin_bit_cast(uint32_t, amax) >> 23) & 255u;
   if (e == 0u || e == 255u) return 1.0f;

@@ -21,6 +21,7 @@ constexpr float kNone = -1e30f;  // reference of a row that has seen nothing
 constexpr int kRowTile = 16;
 constexpr int kWantedGroups = 512;  // two workgroups per CU
 constexpr int kMinBlocks = 16;      // of a split
+constexpr int kOwnSteps = 16;       // attend_few: up to this many steps an item has one workgroup of its own
 constexpr int kStashRows = 8;       // up to this many rows z is kept for the weights
 
 struct AttnParams {
@@ -30,8 +31,8 @@ struct AttnParams {
   float* lse;
   float* weights;
   int64_t wsb, wsh;
-  float* part;      // [batch][kv head][split][row][D] sums, then [..][row][2] (reference, sum of p)
-  float* part_rl;
+  float* part;      // sums of the parts of rows, [part row][D]
+  float* part_rl;   // and their references and sums of p, [part row][2]
   float scale2;     // scale * log2 e
   unsigned gq, gq_inv;  // q heads per kv head, and floor(2^32 / gq), at most 2^32 - 1
   int causal, window, zero_rest;
@@ -41,6 +42,7 @@ struct AttnParams {
   int chunk;        // slots of a split
   int nsplit, tiles, tile_rows;
   int rows;         // tokens * gq
+  int shared;       // attend_few: workgroups that share all steps evenly; 0: one per sequence and head
 };
 
 // The token of a row: row / gq, from the reciprocal, which is at most one short.
@@ -55,11 +57,15 @@ struct Span {
   int ql, rows;     // query tokens and rows of the sequence
   int64_t lo, hi;
 };
-__device__ __forceinline__ void seq_span(const AttnParams& p, int b, Span& s) {
-  const int64_t len = p.c.lengths[b];
+__device__ __forceinline__ void seq_span(const AttnParams& p, int length, int q_len, Span& s) {
+  const int64_t len = length;
   s.len = len < 0 ? 0 : len > p.max_len ? p.max_len : len;
-  s.ql = p.q_lens ? min(max(p.q_lens[b], 0), p.q.tokens) : p.q.tokens;
+  s.ql = min(max(q_len, 0), p.q.tokens);
   s.rows = s.ql * int(p.gq);
+}
+__device__ __forceinline__ int q_len_of(const AttnParams& p, int b) { return p.q_lens ? p.q_lens[b] : p.q.tokens; }
+__device__ __forceinline__ void seq_span(const AttnParams& p, int b, Span& s) {
+  seq_span(p, p.c.lengths[b], q_len_of(p, b), s);
 }
 __device__ __forceinline__ void tile_span(const AttnParams& p, int row0, Span& s) {
   const int last = min(row0 + p.tile_rows, s.rows) - 1;
@@ -178,18 +184,18 @@ __device__ __forceinline__ void join_refs(float* sums, int waves, int rows, int 
   refs[wave * rows + row] = ref;
   refs[(waves + wave) * rows + row] = l;
 }
-// Add them up in a fixed order and write the rows from row0 on: the result
-// where the slots are not split, else the split's part.
+// Add them up in a fixed order and write the rows from row0 on: the result where
+// `all` slots of the rows are in, else the part that starts at part row `at`.
 template <int D, int NW, int ROWS>
-__device__ __forceinline__ void join_waves(const AttnParams& p, const Span& s, const float* sums, int b, int hk, int split,
-                                           int used, int row0) {
+__device__ __forceinline__ void join_waves(const AttnParams& p, const Span& s, const float* sums, int b, int hk, int row0,
+                                           bool all, int64_t at) {
   constexpr int LD = D + 4;
   const float* refs = sums + NW * ROWS * LD;
   const float* ls = refs + NW * ROWS;
   for (int it = threadIdx.x; it < ROWS * (D / 4); it += NW * 64) {
     const int r = it / (D / 4), c = (it % (D / 4)) * 4, row = row0 + r;
     if (row >= s.rows) {
-      if (p.zero_rest && p.nsplit == 1 && row < p.rows)
+      if (p.zero_rest && all && row < p.rows)
         *reinterpret_cast<u2_t*>(out_row(p, b, hk, row) + c) = u2_t{0u, 0u};
       continue;
     }
@@ -203,14 +209,13 @@ __device__ __forceinline__ void join_waves(const AttnParams& p, const Span& s, c
       l = fmaf(ls[w * ROWS + r], f, l);
       o += *reinterpret_cast<const f4_t*>(sums + (w * ROWS + r) * LD + c) * f;
     }
-    const int64_t at = part_row(p, b, hk, split, row);
-    if (p.nsplit == 1) {
+    if (all) {
       put_out(p, b, hk, row, c, o, l);
       if (p.lse && c == 0) put_lse(p, b, hk, row, m, l);
-    } else if (split < used) {
-      *reinterpret_cast<f4_t*>(p.part + at * D + c) = o;
+    } else {
+      *reinterpret_cast<f4_t*>(p.part + (at + r) * D + c) = o;
     }
-    if (p.part_rl && split < used && c == 0) { p.part_rl[at * 2] = m; p.part_rl[at * 2 + 1] = l; }
+    if (p.part_rl && c == 0) { p.part_rl[(at + r) * 2] = m; p.part_rl[(at + r) * 2 + 1] = l; }
   }
 }
 
@@ -261,7 +266,7 @@ __device__ __forceinline__ void wait_loads() {   // until at most N loads of the
 }
 
 template <int D, int G, int NQ>
-__global__ void __launch_bounds__(ring_waves(D) * 64, D == 256 ? 1 : 2) attend_rows(const AttnParams p) {
+__global__ void __launch_bounds__(ring_waves(D) * 64, D == 256 || (G == 4 && NQ == 2) ? 1 : 2) attend_rows(const AttnParams p) {
   typedef Ring<D, G> R;
   constexpr int NK = D / 32, NV = D / 16, KG = NK / G, VG = NV / G, NW = R::NW, DEPTH = R::DEPTH;
   constexpr int CK = kchunk(D), CV = vchunk(D);
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(ring_waves(D) * 64, D == 256 ? 1 : 2) attend_r
   }
   tile_span(p, row0, s);
   const int used = used_splits(p, s);
-  if (split >= used && split > 0) return;   // split 0 writes the zeros of a tile that sees nothing
+  if (split >= used && p.nsplit > 1) return;   // an only split writes the zeros of a tile that sees nothing
   const int64_t begin = s.lo + int64_t(split) * p.chunk, end = min(begin + p.chunk, s.hi);
   const int nblk = end > begin ? int((end - begin + kBlock - 1) / kBlock) : 0;
   const int mine = nblk > wave ? (nblk - wave + NW - 1) / NW : 0;
@@ -463,35 +468,39 @@ __global__ void __launch_bounds__(ring_waves(D) * 64, D == 256 ? 1 : 2) attend_r
         for (int c = 0; c < NV; c++) acc[t][c] *= f;
       }
     }
-    // p s as the sum of two fp16 (22 bits): one alone costs more than the
-    // rounding of an fp16 result, since the code part is cancelled by p lo.
-    h8_t hi[NQ][G], rest[NQ][G];
 #pragma unroll
     for (int t = 0; t < NQ; t++)
 #pragma unroll
       for (int e = 0; e < 8; e++) {
-        const float pe = exp2_fast(z[t][e] - ref[t]);
-        psum[t] += pe;
-#pragma unroll
-        for (int g = 0; g < G; g++) {
-          const h8_t sv = __builtin_bit_cast(h8_t, vs[g]), lv = __builtin_bit_cast(h8_t, vl[g]);
-          plo[t][g] = fmaf(pe, (float)lv[e], plo[t][g]);
-          const float ps = pe * (float)sv[e];
-          hi[t][g][e] = (_Float16)ps;
-          rest[t][g][e] = (_Float16)(ps - (float)hi[t][g][e]);
-        }
+        z[t][e] = exp2_fast(z[t][e] - ref[t]);   // p from here on
+        psum[t] += z[t][e];
       }
+    typename Chunk<CV>::type w[NV / CV];
 #pragma unroll
-    for (int k = 0; k < NV / CV; k++) {
-      const auto w = *reinterpret_cast<const typename Chunk<CV>::type*>(blk + vcode_at(D, G, lane, k * CV));
+    for (int k = 0; k < NV / CV; k++)
+      w[k] = *reinterpret_cast<const typename Chunk<CV>::type*>(blk + vcode_at(D, G, lane, k * CV));
+    // p s as the sum of two fp16 (22 bits): one alone costs more than the
+    // rounding of an fp16 result, since the code part is cancelled by p lo.
 #pragma unroll
-      for (int x = 0; x < CV; x++) {
-        const int c = k * CV + x;
-        const h8_t vf = codes8(w[x]);
+    for (int g = 0; g < G; g++) {
+      const h8_t sv = __builtin_bit_cast(h8_t, vs[g]), lv = __builtin_bit_cast(h8_t, vl[g]);
+      h8_t hi[NQ], rest[NQ];
+#pragma unroll
+      for (int t = 0; t < NQ; t++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          plo[t][g] = fmaf(z[t][e], (float)lv[e], plo[t][g]);
+          const float ps = z[t][e] * (float)sv[e];
+          hi[t][e] = (_Float16)ps;
+          rest[t][e] = (_Float16)(ps - (float)hi[t][e]);
+        }
+#pragma unroll
+      for (int c = g * VG; c < (g + 1) * VG; c++) {
+        const h8_t vf = codes8(w[c / CV][c % CV]);
 #pragma unroll
         for (int t = 0; t < NQ; t++) {
-          acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, hi[t][c / VG], acc[t][c], 0, 0, 0);
-          acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, rest[t][c / VG], acc[t][c], 0, 0, 0);
+          acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, hi[t], acc[t][c], 0, 0, 0);
+          acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, rest[t], acc[t][c], 0, 0, 0);
         }
       }
     }
@@ -513,7 +522,8 @@ __global__ void __launch_bounds__(ring_waves(D) * 64, D == 256 ? 1 : 2) attend_r
     }
     if (set == 0) join_refs(sums, NW, kRowTile, D, wave, n, ref[t], l);
     __syncthreads();
-    join_waves<D, NW, kRowTile>(p, s, sums, b, hk, split, used, row0 + t * kRowTile);
+    join_waves<D, NW, kRowTile>(p, s, sums, b, hk, row0 + t * kRowTile, p.nsplit == 1,
+                                part_row(p, b, hk, split, row0 + t * kRowTile));
   }
 }
 
@@ -533,39 +543,84 @@ constexpr int few_waves(int D) { return D == 256 ? 2 : 4; }
 constexpr int kFewRows = 4;
 constexpr int kFewDepth = 4;   // blocks of a ring
 
+// Steps of a sequence, the same for all its kv heads.
+__device__ __forceinline__ int few_steps(const AttnParams& p, Span& s) {
+  if (s.rows == 0) { s.lo = s.hi = 0; return 0; }
+  tile_span(p, 0, s);
+  return s.hi <= s.lo ? 0 : int((s.hi - s.lo + 2 * kBlock - 1) / (2 * kBlock));
+}
+__device__ __forceinline__ int few_steps(const AttnParams& p, int b) {
+  Span s;
+  seq_span(p, b, s);
+  return few_steps(p, s);
+}
+__device__ __forceinline__ int prefix64(int v) {   // inclusive, over the wave
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(v, d);
+    if (int(threadIdx.x & 63) >= d) v += o;
+  }
+  return v;
+}
+// Where lengths differ, the host (which does not know them) cannot cut the work
+// evenly: all steps of all sequences and heads are numbered, and workgroup w
+// takes the `quota` from w quota on, across heads and sequences.  Beginning an
+// item (sequence, head) takes as long as some steps: it is charged kItemCost
+// numbers after its last step (without them a workgroup that met ten heads of a
+// one-token sequence took 59 us where the others took 15).  An item that starts
+// at number `first` and has n > 0 steps is in the workgroups first / quota ..
+// (first + n - 1) / quota, and its part in workgroup w is part w + item, which
+// no two parts share.
+struct Shares {
+  int total, quota;
+};
+constexpr int kMinQuota = 16;  // steps: four per wave
+constexpr int kItemCost = 8;
+__device__ __forceinline__ int few_cost(const AttnParams& p, int b) {
+  const int n = few_steps(p, b);
+  return n > 0 ? n + kItemCost : 0;
+}
+__device__ __forceinline__ Shares few_shares(const AttnParams& p, int total) {
+  const int q = int((unsigned(total) + unsigned(p.shared) - 1) / unsigned(p.shared));
+  return Shares{total, q < kMinQuota ? kMinQuota : q};
+}
+// First number of sequence b (b may be the batch: the total).
+__device__ __forceinline__ int few_first(const AttnParams& p, int b) {
+  int sum = 0;
+  for (int b0 = 0; b0 < b; b0 += 64) {
+    const int i = b0 + (threadIdx.x & 63);
+    int v = i < b ? few_cost(p, i) * p.c.heads : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    sum += __builtin_amdgcn_readfirstlane(v);
+  }
+  return sum;
+}
+
+// LDS of attend_few: the waves' rings (later their sums), then a copy of the
+// query rows per wave.
 template <int D, int G>
-__global__ void __launch_bounds__(few_waves(D) * 64, D == 256 ? 1 : 2) attend_few(const AttnParams p) {
+struct FewLds {
+  static constexpr uint32_t RING = few_waves(D) * kFewDepth * block_bytes(D, G);
+  static constexpr uint32_t JOIN = join_bytes(few_waves(D), kFewRows, D);
+  static constexpr uint32_t Q = RING > JOIN ? RING : JOIN;
+  static constexpr uint32_t BYTES = Q + few_waves(D) * kFewRows * D * 2;
+};
+
+// `steps` steps from step `first` of one sequence and kv head.
+template <int D, int G>
+__device__ __forceinline__ void few_segment(const AttnParams& p, const Span& s, int b, int hk, int first, int steps, bool all,
+                                            int64_t at_part, uint8_t* lds) {
   constexpr int NW = few_waves(D), NK = D / 32, NH = D / 64, KG = NK / G, CK = kchunk(D), LD = D + 4;
   constexpr uint32_t BB = block_bytes(D, G);
   constexpr int LOADS = 2 * int((BB + 1023) / 1024);   // of a wave per step
-  constexpr uint32_t RING = NW * kFewDepth * BB, JOIN = join_bytes(NW, kFewRows, D);
-  __shared__ __attribute__((aligned(16))) uint8_t lds[RING > JOIN ? RING : JOIN];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // (opaque, so that what hangs on it is not kept in registers across segments)
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int j = lane & 3, quad = lane >> 2;   // row, and set of four slots of the step
-  const int split = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
-  // the row, and (bf16) a lane's part of it for its largest magnitude: requested
-  // before anything that depends on the lengths
-  constexpr int PART = (D / 8 + 15) / 16;
-  u4_t raw[D / 8], part[PART];
-  {
-    const u4_t* src = reinterpret_cast<const u4_t*>(q_row(p, b, hk, min(j, p.rows - 1)));
-#pragma unroll
-    for (int c = 0; c < D / 8; c++) raw[c] = src[c];
-#pragma unroll
-    for (int c = 0; c < PART; c++) part[c] = src[(c * 16 + quad) % (D / 8)];
-  }
-  Span s;
-  seq_span(p, b, s);
-  if (s.rows == 0) {
-    if (p.zero_rest && p.nsplit == 1) zero_rows<D>(p, b, hk, 0, p.rows);
-    return;
-  }
-  tile_span(p, 0, s);
-  const int used = used_splits(p, s);
-  if (split >= used && split > 0) return;   // split 0 writes the zeros of rows that see nothing
-  const int64_t begin = s.lo + int64_t(split) * p.chunk, end = min(begin + p.chunk, s.hi);
-  const int nstep = end > begin ? int((end - begin + 2 * kBlock - 1) / (2 * kBlock)) : 0;
-  const int mine = nstep > wave ? (nstep - wave + NW - 1) / NW : 0;
+  const int64_t begin = s.lo + int64_t(first) * 2 * kBlock, end = min(begin + int64_t(steps) * 2 * kBlock, s.hi);
+  const int mine = steps > wave ? (steps - wave + NW - 1) / NW : 0;
 
   // lane i holds the page of the wave's block i (two per step); -1: none
   int page = -1;
@@ -589,20 +644,45 @@ __global__ void __launch_bounds__(few_waves(D) * 64, D == 256 ? 1 : 2) attend_fe
   };
   if (mine > 0) fetch(0);
 
-  // q of row j, all channels (lanes of one row hold the same)
-  h8_t qf[D / 8];
+  // The rows come in once per wave, CH lanes a row, are scaled (bf16) and turned
+  // through LDS: lane j + 4 n then holds row j.
+  constexpr int CH = D / 8, LOADQ = kFewRows * CH > 64 ? kFewRows * CH / 64 : 1;
+  h8_t qf[CH];
   float qsum[G], z_unit = p.scale2 * kCodeUnit;
   const bool there = j < s.rows;
-  if (p.q.dtype == STAGQ_F16) {
+  {
+    h8_t* stage = reinterpret_cast<h8_t*>(lds + FewLds<D, G>::Q) + wave * kFewRows * CH;
+    u4_t raw[LOADQ];
 #pragma unroll
-    for (int c = 0; c < D / 8; c++) qf[c] = __builtin_bit_cast(h8_t, raw[c]);
-  } else {
-    const float m = row_scale(max_quads(amax_bf16<PART>(part)));
-    bf16_to_half<D / 8>(raw, m, qf);
-    z_unit /= m;
+    for (int i = 0; i < LOADQ; i++) {
+      const int row = (i * 64 + lane) / CH, ch = lane % CH;
+      raw[i] = u4_t{0u, 0u, 0u, 0u};
+      if (row < min(s.rows, kFewRows)) raw[i] = *reinterpret_cast<const u4_t*>(q_row(p, b, hk, row) + ch * 16);
+    }
+    float unit[kFewRows];
+#pragma unroll
+    for (int i = 0; i < LOADQ; i++) {
+      const int row = (i * 64 + lane) / CH, ch = lane % CH;
+      h8_t h = __builtin_bit_cast(h8_t, raw[i]);
+      float m = 1.0f;
+      if (p.q.dtype != STAGQ_F16) {
+        float amax = amax_bf16<1>(&raw[i]);
+#pragma unroll
+        for (int d = 1; d < CH; d *= 2) amax = fmaxf(amax, __shfl_xor(amax, d));
+        m = row_scale(amax);
+        bf16_to_half<1>(&raw[i], m, &h);
+      }
+#pragma unroll
+      for (int r = i * 64 / CH; r < (i + 1) * 64 / CH && r < kFewRows; r++)
+        unit[r] = 1.0f / __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, m), r * CH - i * 64));
+      if (row < kFewRows) stage[row * CH + ch] = h;
+    }
+    z_unit *= j == 0 ? unit[0] : j == 1 ? unit[1] : j == 2 ? unit[2] : unit[3];
+#pragma unroll
+    for (int c = 0; c < CH; c++) qf[c] = stage[j * CH + c];
   }
 #pragma unroll
-  for (int g = 0; g < G; g++) qsum[g] = sum8<D / 8 / G>(qf + g * (D / 8 / G)) * (1.0f / kCodeUnit);
+  for (int g = 0; g < G; g++) qsum[g] = sum8<CH / G>(qf + g * (CH / G)) * (1.0f / kCodeUnit);
   int64_t from = 0, to = 0;
   if (there) row_span(p, s, j, from, to);
   int64_t all_from, all_to;   // slots that every row sees
@@ -760,7 +840,92 @@ __global__ void __launch_bounds__(few_waves(D) * 64, D == 256 ? 1 : 2) attend_fe
     }
   if (quad == 0) join_refs(sums, NW, kFewRows, D, wave, j, ref, l);
   __syncthreads();
-  join_waves<D, NW, kFewRows>(p, s, sums, b, hk, split, used, 0);
+  join_waves<D, NW, kFewRows>(p, s, sums, b, hk, 0, all, at_part);
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(few_waves(D) * 64, D == 256 ? 1 : 2) attend_few(const AttnParams p) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[FewLds<D, G>::BYTES];
+  const int lane = threadIdx.x & 63, w = blockIdx.x;
+  const bool own = p.shared == 0;
+  int pos = 0, end = 1;
+  // sequences in sets of 64: `seen` numbers before the set; lane i's sequence has
+  // this length, this many rows, and ends at number seen + upto
+  int set = 0, seen = 0, length = 0, q_len = 0, cost = 0, upto = 0;
+  auto look = [&](int from) {
+    length = q_len = 0;
+    if (from + lane < p.c.batch) {
+      length = p.c.lengths[from + lane];
+      q_len = q_len_of(p, from + lane);
+    }
+    Span s;
+    seq_span(p, length, q_len, s);
+    const int n = few_steps(p, s);
+    cost = n > 0 ? n + kItemCost : 0;
+    upto = prefix64(cost * p.c.heads);
+  };
+  if (!own) {
+    look(0);
+    int total = __builtin_amdgcn_readlane(upto, 63);
+    if (p.c.batch > 64) total = few_first(p, p.c.batch);
+    const Shares sh = few_shares(p, total);
+    pos = w * sh.quota;   // below 2^31, see plan
+    end = min(sh.total - pos, sh.quota) + pos;
+  }
+  bool more = false;
+#pragma unroll 1
+  while (pos < end) {
+    int b = blockIdx.z, hk = blockIdx.y, first = 0, take, n;
+    int64_t part = (int64_t(b) * p.c.heads + hk) * kFewRows;
+    Span s;
+    if (own) {
+      seq_span(p, b, s);
+      take = n = few_steps(p, s);
+      pos = end;
+    } else {
+      int in_set = __builtin_amdgcn_readlane(upto, 63);
+      while (pos - seen >= in_set) {
+        seen += in_set;
+        set += 64;
+        look(set);
+        in_set = __builtin_amdgcn_readlane(upto, 63);
+      }
+      const int i = __builtin_amdgcn_readfirstlane(__ffsll(__ballot(upto > pos - seen)) - 1);
+      const int c = __builtin_amdgcn_readlane(cost, i);
+      const int into = pos - seen - (__builtin_amdgcn_readlane(upto, i) - c * p.c.heads);   // of the sequence's numbers
+      seq_span(p, __builtin_amdgcn_readlane(length, i), __builtin_amdgcn_readlane(q_len, i), s);
+      n = few_steps(p, s);
+      b = set + i;
+      hk = into / c;
+      first = into - hk * c;
+      take = min(c - first, end - pos);
+      part = (int64_t(w) + int64_t(b) * p.c.heads + hk) * kFewRows;
+      pos += take;
+      take = min(take, n - first);
+      if (take <= 0) continue;   // what was left of the item is its charge
+    }
+    if (more) __syncthreads();   // the last segment's sums have been read
+    few_segment<D, G>(p, s, b, hk, first, take, take == n, part, lds);
+    more = true;
+  }
+}
+
+// The parts that make up the rows of a sequence and kv head: `count` of them,
+// part k's row r at first + k stride + r.  done: the rows are written already.
+struct Parts {
+  int64_t first, stride;
+  int count;
+  bool done;
+};
+__device__ __forceinline__ Parts parts_of(const AttnParams& p, const Span& s, int b, int hk) {
+  if (p.tile_rows != kFewRows) return Parts{part_row(p, b, hk, 0, 0), p.rows, used_splits(p, s), p.nsplit == 1};
+  const int64_t item = int64_t(b) * p.c.heads + hk;
+  const int n = few_steps(p, b);
+  if (p.shared == 0) return Parts{item * kFewRows, kFewRows, n > 0 ? 1 : 0, true};
+  if (n == 0) return Parts{0, 0, 0, false};
+  const Shares sh = few_shares(p, few_first(p, p.c.batch));
+  const int first = few_first(p, b) + hk * (n + kItemCost), w0 = first / sh.quota, w1 = (first + n - 1) / sh.quota;
+  return Parts{(w0 + item) * kFewRows, kFewRows, w1 - w0 + 1, w0 == w1};
 }
 
 // Join the splits of a row, in a fixed order: D / 4 lanes hold the row, and the
@@ -777,11 +942,13 @@ __device__ __forceinline__ void join_row(const AttnParams& p, unsigned id, float
     return;
   }
   tile_span(p, row / p.tile_rows * p.tile_rows, s);
-  const int used = used_splits(p, s);
-  const int64_t first = part_row(p, b, hk, 0, row);
+  const Parts parts = parts_of(p, s, b, hk);
+  if (parts.done) return;
+  const int used = parts.count;
+  const int64_t first = parts.first + row;
   const int lane = threadIdx.x & 63, group = threadIdx.x / LV, c = (threadIdx.x % LV) * 4;
   float m = kNone;
-  for (int i = lane; i < used; i += 64) m = fmaxf(m, p.part_rl[(first + int64_t(i) * p.rows) * 2]);
+  for (int i = lane; i < used; i += 64) m = fmaxf(m, p.part_rl[(first + i * parts.stride) * 2]);
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
   float l = 0.0f;
@@ -789,7 +956,7 @@ __device__ __forceinline__ void join_row(const AttnParams& p, unsigned id, float
   if (group < NG)
 #pragma unroll 4
     for (int i = group; i < used; i += NG) {
-      const int64_t at = first + int64_t(i) * p.rows;
+      const int64_t at = first + i * parts.stride;
       const float f = exp2_fast(p.part_rl[at * 2] - m);
       l = fmaf(p.part_rl[at * 2 + 1], f, l);
       o += *reinterpret_cast<const f4_t*>(p.part + at * D + c) * f;
@@ -818,18 +985,19 @@ __device__ __forceinline__ void weigh_stash(const AttnParams& p, unsigned id, fl
   seq_span(p, b, s);
   if (s.rows == 0) return;
   tile_span(p, 0, s);
-  const int used = used_splits(p, s);
+  const Parts parts = parts_of(p, s, b, hk);
+  const int used = parts.count;
   if (slot - threadIdx.x * 4 >= s.hi || used == 0) return;
   // the rows' log-sum-exp: 32 lanes per row (at most 8 rows)
   const int r = threadIdx.x >> 5, l32 = threadIdx.x & 31;
   float m = kNone, l = 0.0f;
   if (r < s.rows) {
-    const int64_t first = part_row(p, b, hk, 0, r);
-    for (int i = l32; i < used; i += 32) m = fmaxf(m, p.part_rl[(first + int64_t(i) * p.rows) * 2]);
+    const int64_t first = parts.first + r;
+    for (int i = l32; i < used; i += 32) m = fmaxf(m, p.part_rl[(first + i * parts.stride) * 2]);
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
     for (int i = l32; i < used; i += 32) {
-      const int64_t at = (first + int64_t(i) * p.rows) * 2;
+      const int64_t at = (first + i * parts.stride) * 2;
       l = fmaf(p.part_rl[at + 1], exp2_fast(p.part_rl[at] - m), l);
     }
 #pragma unroll
@@ -946,7 +1114,7 @@ __global__ void __launch_bounds__(256) weigh_kernel(const AttnParams p) {
 
 // ------------------------------------------------------------- dispatch ----
 struct Plan {
-  int nq, tile_rows, tiles, chunk, nsplit;   // nq 0: attend_few
+  int nq, tile_rows, tiles, chunk, nsplit, shared;   // nq 0: attend_few
   bool stash;
   int64_t stash_len, groups, joins, weighs;
   size_t part, rl, lse, z, total;   // offsets in the workspace, its size
@@ -958,41 +1126,57 @@ static bool plan(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv
   const int64_t rows = int64_t(a->q.tokens) * gq;
   if (rows > (int64_t(1) << 30)) return false;
   const int waves = ring_waves(c->head_dim);
-  const bool few = rows <= kFewRows && c->group >= 64;   // a set of 64 channels shares its pair there
+  const int64_t all = c->pages > 0 ? reach(c, q, a->max_len) : 0;   // without pages there is nothing to see
+  const int64_t heads = int64_t(q->batch) * c->kv_heads;
+  auto spanned = [&](int tile_rows) {   // slots a tile's rows see at most, from the start of two blocks
+    const int64_t most = int64_t(a->window) + (tile_rows + gq - 1) / gq + 1 + 2 * kBlock;
+    return a->window > 0 && most < all ? most : all;
+  };
+  // attend_few: a set of 64 channels has to share its pair; step numbers are below 2^30
+  const int64_t steps = (spanned(kFewRows) + 2 * kBlock - 1) / (2 * kBlock), cost = steps + kItemCost;
+  const bool few = rows <= kFewRows && c->group >= 64 && heads * cost < (int64_t(1) << 30);
   pl->nq = few ? 0 : rows > kRowTile && c->head_dim < 256 ? 2 : 1;
   pl->tile_rows = few ? kFewRows : pl->nq * kRowTile;
   pl->tiles = int((rows + pl->tile_rows - 1) / pl->tile_rows);
-  const int64_t all = c->pages > 0 ? reach(c, q, a->max_len) : 0;   // without pages there is nothing to see
-  int64_t span = all;
-  if (a->window > 0) {   // a tile's rows see at most this many slots, from the start of two blocks
-    const int64_t most = int64_t(a->window) + (pl->tile_rows + gq - 1) / gq + 1 + 2 * kBlock;
-    span = most < span ? most : span;
-  }
-  const int64_t blocks = (span + kBlock - 1) / kBlock;
-  const int64_t heads = int64_t(q->batch) * c->kv_heads;
   const int64_t base = heads * pl->tiles;
-  const int64_t wanted = base > 0 ? (kWantedGroups + base - 1) / base : 1;
-  int64_t per = (blocks + wanted - 1) / wanted;
-  per = per < kMinBlocks ? kMinBlocks : per > 64 * waves ? 64 * waves : per;   // 64 blocks per wave at most
-  per = (per + 2 * waves - 1) / (2 * waves) * (2 * waves);
-  pl->chunk = int(per) * kBlock;
-  pl->nsplit = int(blocks ? (blocks + per - 1) / per : 1);
-  pl->groups = base * pl->nsplit;
+  pl->shared = 0;
+  pl->nsplit = pl->chunk = 1;
+  size_t part_rows;
+  if (few) {
+    // one workgroup per item up to kOwnSteps steps; beyond, the grid shares all
+    // steps, at most 32 per wave (a page-table entry per lane and block)
+    if (steps > kOwnSteps) {
+      const int64_t most = few_waves(c->head_dim) * 32, need = (heads * cost + most - 1) / most;
+      pl->shared = int(need > kWantedGroups ? need : kWantedGroups);
+    }
+    part_rows = size_t(pl->shared + heads) * kFewRows;
+    pl->groups = pl->shared ? pl->shared : heads;
+  } else {
+    const int64_t blocks = (spanned(pl->tile_rows) + kBlock - 1) / kBlock;
+    const int64_t wanted = base > 0 ? (kWantedGroups + base - 1) / base : 1;
+    int64_t per = (blocks + wanted - 1) / wanted;
+    per = per < kMinBlocks ? kMinBlocks : per > 64 * waves ? 64 * waves : per;   // 64 blocks per wave at most
+    per = (per + waves - 1) / waves * waves;
+    pl->chunk = int(per) * kBlock;
+    pl->nsplit = int(blocks ? (blocks + per - 1) / per : 1);
+    part_rows = size_t(heads) * pl->nsplit * size_t(rows);
+    pl->groups = base * pl->nsplit;
+  }
+  const bool split = pl->nsplit > 1 || pl->shared > 0;
   pl->stash = a->weights && rows <= kStashRows;
   pl->stash_len = (all + kBlock - 1) / kBlock * kBlock;
-  pl->joins = pl->nsplit > 1 ? heads * rows : 0;
+  pl->joins = split ? heads * rows : 0;
   pl->weighs = !a->weights ? 0 : pl->stash ? heads * ((all + 1023) / 1024) : heads * ((all + 4 * kBlock - 1) / (4 * kBlock));
   if (q->batch > 65535 || int64_t(pl->tiles) * c->kv_heads > 65535) return false;   // y and z of the grid
   if (!launchable(pl->groups, 256) || !launchable(pl->joins + pl->weighs, 256)) return false;
-  const size_t rows_all = size_t(heads) * pl->nsplit * size_t(rows);
   size_t o = 0;
   auto take = [&](bool used, size_t bytes) {
     const size_t at = o;
     if (used) o += (bytes + 255) / 256 * 256;
     return at;
   };
-  pl->part = take(pl->nsplit > 1, rows_all * c->head_dim * 4);
-  pl->rl = take(pl->nsplit > 1 || pl->stash, rows_all * 8);
+  pl->part = take(split, part_rows * c->head_dim * 4);
+  pl->rl = take(split || pl->stash, part_rows * 8);
   pl->lse = take(a->weights && !pl->stash && !a->lse, size_t(q->batch) * a->q.tokens * a->q.heads * 4);
   pl->z = take(pl->stash, size_t(heads) * rows * pl->stash_len * 4);
   pl->total = o;
@@ -1007,7 +1191,8 @@ struct LaunchAttention {
   int go() {
     const dim3 grid(unsigned(pl.nsplit), unsigned(pl.tiles * p.c.heads), unsigned(p.c.batch)), threads(Ring<D, G>::NW * 64);
     if constexpr (D / G >= 64) {
-      if (pl.nq == 0) hipLaunchKernelGGL((attend_few<D, G>), grid, dim3(few_waves(D) * 64), 0, st, p);
+      const dim3 shares = p.shared ? dim3(unsigned(p.shared)) : grid;
+      if (pl.nq == 0) hipLaunchKernelGGL((attend_few<D, G>), shares, dim3(few_waves(D) * 64), 0, st, p);
     }
     if (pl.nq == 0) {
     } else if constexpr (D < 256) {
@@ -1083,7 +1268,7 @@ int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
   p.wsb = a->weights_stride_seq;
   p.wsh = a->weights_stride_head;
   p.part = reinterpret_cast<float*>(ws + pl.part);
-  p.part_rl = pl.nsplit > 1 || pl.stash ? reinterpret_cast<float*>(ws + pl.rl) : nullptr;
+  p.part_rl = pl.nsplit > 1 || pl.shared > 0 || pl.stash ? reinterpret_cast<float*>(ws + pl.rl) : nullptr;
   p.stash = pl.stash ? reinterpret_cast<float*>(ws + pl.z) : nullptr;
   p.stash_len = pl.stash_len;
   p.zero_rest = a->zero_rest != 0;
@@ -1095,6 +1280,7 @@ int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
   p.max_len = c->pages > 0 ? reach(c, q, a->max_len) : 0;
   p.chunk = pl.chunk;
   p.nsplit = pl.nsplit;
+  p.shared = pl.shared;
   p.tiles = pl.tiles;
   p.tile_rows = pl.tile_rows;
   p.rows = a->q.tokens * int(p.gq);

@@ -43,6 +43,7 @@ struct AttnParams {
   int nsplit, tiles, tile_rows;
   int rows;         // tokens * gq
   int shared;       // attend_few: workgroups that share all steps evenly; 0: one per sequence and head
+  int2* where;      // then, by sequence and head: its first part and their number
 };
 
 // The token of a row: row / gq, from the reciprocal, which is at most one short.
@@ -571,25 +572,18 @@ __device__ __forceinline__ int prefix64(int v) {   // inclusive, over the wave
 // at number `first` and has n > 0 steps is in the workgroups first / quota ..
 // (first + n - 1) / quota, and its part in workgroup w is part w + item, which
 // no two parts share.
-struct Shares {
-  int total, quota;
-};
 constexpr int kMinQuota = 16;  // steps: four per wave
 constexpr int kItemCost = 8;
 __device__ __forceinline__ int few_cost(const AttnParams& p, int b) {
   const int n = few_steps(p, b);
   return n > 0 ? n + kItemCost : 0;
 }
-__device__ __forceinline__ Shares few_shares(const AttnParams& p, int total) {
-  const int q = int((unsigned(total) + unsigned(p.shared) - 1) / unsigned(p.shared));
-  return Shares{total, q < kMinQuota ? kMinQuota : q};
-}
-// First number of sequence b (b may be the batch: the total).
-__device__ __forceinline__ int few_first(const AttnParams& p, int b) {
+// Numbers of all sequences.
+__device__ __forceinline__ int few_total(const AttnParams& p) {
   int sum = 0;
-  for (int b0 = 0; b0 < b; b0 += 64) {
-    const int i = b0 + (threadIdx.x & 63);
-    int v = i < b ? few_cost(p, i) * p.c.heads : 0;
+  for (int b0 = 0; b0 < p.c.batch; b0 += 64) {
+    const int b = b0 + (threadIdx.x & 63);
+    int v = b < p.c.batch ? few_cost(p, b) * p.c.heads : 0;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
     sum += __builtin_amdgcn_readfirstlane(v);
@@ -848,7 +842,7 @@ __global__ void __launch_bounds__(few_waves(D) * 64, D == 256 ? 1 : 2) attend_fe
   __shared__ __attribute__((aligned(16))) uint8_t lds[FewLds<D, G>::BYTES];
   const int lane = threadIdx.x & 63, w = blockIdx.x;
   const bool own = p.shared == 0;
-  int pos = 0, end = 1;
+  int pos = 0, end = 1, quota = 1;
   // sequences in sets of 64: `seen` numbers before the set; lane i's sequence has
   // this length, this many rows, and ends at number seen + upto
   int set = 0, seen = 0, length = 0, q_len = 0, cost = 0, upto = 0;
@@ -867,10 +861,10 @@ __global__ void __launch_bounds__(few_waves(D) * 64, D == 256 ? 1 : 2) attend_fe
   if (!own) {
     look(0);
     int total = __builtin_amdgcn_readlane(upto, 63);
-    if (p.c.batch > 64) total = few_first(p, p.c.batch);
-    const Shares sh = few_shares(p, total);
-    pos = w * sh.quota;   // below 2^31, see plan
-    end = min(sh.total - pos, sh.quota) + pos;
+    if (p.c.batch > 64) total = few_total(p);
+    quota = max(int((unsigned(total) + unsigned(p.shared) - 1) / unsigned(p.shared)), kMinQuota);
+    pos = w * quota;   // below 2^31, see plan
+    end = min(total - pos, quota) + pos;
   }
   bool more = false;
 #pragma unroll 1
@@ -899,7 +893,9 @@ __global__ void __launch_bounds__(few_waves(D) * 64, D == 256 ? 1 : 2) attend_fe
       hk = into / c;
       first = into - hk * c;
       take = min(c - first, end - pos);
-      part = (int64_t(w) + int64_t(b) * p.c.heads + hk) * kFewRows;
+      const int64_t item = int64_t(b) * p.c.heads + hk;
+      part = (w + item) * kFewRows;
+      if (first == 0 && threadIdx.x == 0) p.where[item] = int2{int(w + item), (pos + n - 1) / quota - w + 1};
       pos += take;
       take = min(take, n - first);
       if (take <= 0) continue;   // what was left of the item is its charge
@@ -923,9 +919,8 @@ __device__ __forceinline__ Parts parts_of(const AttnParams& p, const Span& s, in
   const int n = few_steps(p, b);
   if (p.shared == 0) return Parts{item * kFewRows, kFewRows, n > 0 ? 1 : 0, true};
   if (n == 0) return Parts{0, 0, 0, false};
-  const Shares sh = few_shares(p, few_first(p, p.c.batch));
-  const int first = few_first(p, b) + hk * (n + kItemCost), w0 = first / sh.quota, w1 = (first + n - 1) / sh.quota;
-  return Parts{(w0 + item) * kFewRows, kFewRows, w1 - w0 + 1, w0 == w1};
+  const int2 at = p.where[item];
+  return Parts{int64_t(at.x) * kFewRows, kFewRows, at.y, at.y == 1};
 }
 
 // Join the splits of a row, in a fixed order: D / 4 lanes hold the row, and the
@@ -1117,7 +1112,7 @@ struct Plan {
   int nq, tile_rows, tiles, chunk, nsplit, shared;   // nq 0: attend_few
   bool stash;
   int64_t stash_len, groups, joins, weighs;
-  size_t part, rl, lse, z, total;   // offsets in the workspace, its size
+  size_t part, rl, lse, z, where, total;   // offsets in the workspace, its size
 };
 
 // Variants and splits by shape alone.
@@ -1179,6 +1174,7 @@ static bool plan(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv
   pl->rl = take(split || pl->stash, part_rows * 8);
   pl->lse = take(a->weights && !pl->stash && !a->lse, size_t(q->batch) * a->q.tokens * a->q.heads * 4);
   pl->z = take(pl->stash, size_t(heads) * rows * pl->stash_len * 4);
+  pl->where = take(pl->shared > 0, size_t(heads) * sizeof(int2));
   pl->total = o;
   return true;
 }
@@ -1281,6 +1277,7 @@ int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
   p.chunk = pl.chunk;
   p.nsplit = pl.nsplit;
   p.shared = pl.shared;
+  p.where = reinterpret_cast<int2*>(ws + pl.where);
   p.tiles = pl.tiles;
   p.tile_rows = pl.tile_rows;
   p.rows = a->q.tokens * int(p.gq);

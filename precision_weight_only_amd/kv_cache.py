@@ -23,6 +23,10 @@ import torch
 
 from ._lib import check, lib
 
+# the current device and its current stream as a pointer, without building objects (about 2 us a call)
+_device_index = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 _I32, _F32 = torch.int32, torch.float32
 # the structs of include/stagq.h, in their layout
@@ -101,6 +105,8 @@ class KVCache:
         self.head_dim, self.group, self.nbytes = int(head_dim), int(group), n
         self._c = _CACHE.pack(*shape, buffer.data_ptr(), buffer.numel())
         self._scale = 1.0 / math.sqrt(self.head_dim)
+        self._lib = lib()
+        self._needs = {}   # workspace bytes of attention by everything they depend on
 
     # ------------------------------------------------------------ marshalling
     def _seqs(self, what, table, lengths):
@@ -163,17 +169,14 @@ class KVCache:
         """call(stream pointer) with the cache's device, and the given stream, current."""
         index = self.device.index
         if stream is None:
-            if torch.cuda.current_device() == index:
-                return call(torch.cuda.current_stream(index).cuda_stream)
+            if _device_index() == index:
+                return call(_raw_stream(index))
             with _On(self.device, None):
-                return call(torch.cuda.current_stream(index).cuda_stream)
+                return call(_raw_stream(index))
         if stream.device != self.device:
             raise ValueError(f"stream is on {stream.device}, the cache on {self.device}")
         with _On(self.device, stream):
             return call(stream.cuda_stream)
-
-    def _workspace(self, need):
-        return torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
 
     # ------------------------------------------------------------- operators
     def append(self, k, v, table, lengths, new_lens=None, stream=None) -> None:
@@ -187,7 +190,7 @@ class KVCache:
         if k.dtype != v.dtype:
             raise ValueError(f"append: k is {k.dtype}, v {v.dtype}")
         new = self._vector("append", "new_lens", new_lens, B)
-        self._run(stream, lambda st: check(lib().stagq_kv_append(self._c, seqs, kt, vt, new, st), "stagq_kv_append"))
+        self._run(stream, lambda st: check(self._lib.stagq_kv_append(self._c, seqs, kt, vt, new, st), "stagq_kv_append"))
 
     def read(self, table, lengths, tokens: Optional[int] = None, start=None, dtype=None, k=None, v=None,
              stream=None) -> Tuple:
@@ -206,13 +209,20 @@ class KVCache:
             nonlocal k, v
             fresh = k is None
             if fresh:
-                both = torch.empty((2, B, tokens, self.kv_heads, self.head_dim), dtype=dtype or _F32, device=self.device)
-                k, v = both[0], both[1]
-            _, _, kt = self._rows("read", "k", k, B, tokens, self.kv_heads)
-            _, _, vt = self._rows("read", "v", v, B, tokens, self.kv_heads)
-            if k.dtype != v.dtype:
-                raise ValueError(f"read: k is {k.dtype}, v {v.dtype}")
-            check(lib().stagq_kv_read(self._c, seqs, at, kt, vt, 1 if fresh else 0, st), "stagq_kv_read")
+                kind = dtype or _F32
+                if kind not in _DTYPES:
+                    raise ValueError(f"read: dtype must be float16, bfloat16 or float32, not {kind}")
+                h, d = self.kv_heads, self.head_dim
+                both = torch.empty((2, B, tokens, h, d), dtype=kind, device=self.device)
+                k, v = both.unbind(0)
+                rest = (_DTYPES[kind], tokens, h, 0, tokens * h * d, h * d, d)
+                kt, vt = _TENSOR.pack(k.data_ptr(), *rest), _TENSOR.pack(v.data_ptr(), *rest)
+            else:
+                _, _, kt = self._rows("read", "k", k, B, tokens, self.kv_heads)
+                _, _, vt = self._rows("read", "v", v, B, tokens, self.kv_heads)
+                if k.dtype != v.dtype:
+                    raise ValueError(f"read: k is {k.dtype}, v {v.dtype}")
+            check(self._lib.stagq_kv_read(self._c, seqs, at, kt, vt, 1 if fresh else 0, st), "stagq_kv_read")
             return k, v
 
         return self._run(stream, call)
@@ -252,15 +262,24 @@ class KVCache:
             fresh = out is None
             if fresh:
                 out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-            _, _, ot = self._rows("attention", "out", out, B, n, heads, False)
-            if out.dtype != q.dtype:
-                raise ValueError(f"attention: q is {q.dtype}, out {out.dtype}")
+                d = self.head_dim
+                ot = _TENSOR.pack(out.data_ptr(), _DTYPES[q.dtype], n, heads, 0, n * heads * d, heads * d, d)
+            else:
+                _, _, ot = self._rows("attention", "out", out, B, n, heads, False)
+                if out.dtype != q.dtype:
+                    raise ValueError(f"attention: q is {q.dtype}, out {out.dtype}")
             a = qt + ot + _ATTN_REST.pack(ql, ls, w, wb, wh, self._scale if scale is None else scale,
                                           1 if causal else 0, window, reach, 1 if fresh and ql else 0, 0)
-            need = lib().stagq_kv_attention_workspace(self._c, seqs, a)
-            ws = self._workspace(need)
-            check(lib().stagq_kv_attention(self._c, seqs, a, ws.data_ptr() if need else 0, need, st),
-                  "stagq_kv_attention")
+            key = (B, n, heads, window, reach, ls != 0, w != 0)
+            need = self._needs.get(key)
+            if need is None:
+                need = self._lib.stagq_kv_attention_workspace(self._c, seqs, a)
+                if len(self._needs) < 4096:
+                    self._needs[key] = need
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device).data_ptr() if need else 0
+            status = self._lib.stagq_kv_attention(self._c, seqs, a, ws, need, st)
+            if status:
+                check(status, "stagq_kv_attention")
             return out
 
         return self._run(stream, call)
@@ -310,9 +329,9 @@ class KVCache:
                 out_lengths = torch.empty(B, dtype=_I32, device=self.device)
             e = _EVICT.pack(w, o, wb, wh, ob, oh, kept.data_ptr(), self._vector("evict", "out_lengths", out_lengths, B),
                             ot, os_, ow, keep, sinks, recent, reach, 0)
-            need = lib().stagq_kv_evict_workspace(self._c, seqs, e)
-            ws = self._workspace(need)
-            check(lib().stagq_kv_evict(self._c, seqs, e, ws.data_ptr() if need else 0, need, st), "stagq_kv_evict")
+            need = 0 if ot else self._lib.stagq_kv_evict_workspace(self._c, seqs, e)
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+            check(self._lib.stagq_kv_evict(self._c, seqs, e, ws.data_ptr() if need else 0, need, st), "stagq_kv_evict")
             return kept, out_lengths
 
         return self._run(stream, call)

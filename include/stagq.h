@@ -337,7 +337,7 @@ typedef struct {
  * counts the tokens of the call too (append: after it). */
 typedef struct {
   int32_t batch;
-  int32_t table_width;        /* entries of a row of the table */
+  int32_t table_width;        /* entries of a row of the table; width * page_tokens <= 2^30 */
   int64_t table_stride;       /* int32 elements from one row to the next */
   const int32_t* table;       /* 4-byte aligned */
   const int32_t* lengths;     /* [batch] */

@@ -21,6 +21,8 @@ constexpr float kNone = -1e30f;  // reference of a row that has seen nothing
 constexpr int kRowTile = 16;
 constexpr int kWantedGroups = 512;  // two workgroups per CU
 constexpr int kMinBlocks = 16;      // of a split
+constexpr int kMinTileBlocks = 16;  // of a split of attend_tiles
+constexpr int kManyRows = 32;       // beyond, attend_tiles
 constexpr int kOwnSteps = 16;       // attend_few: up to this many steps an item has one workgroup of its own
 constexpr int kStashRows = 8;       // up to this many rows z is kept for the weights
 
@@ -38,6 +40,9 @@ struct AttnParams {
   int causal, window, zero_rest;
   float* stash;     // or z (binary orders) of [batch][kv head][row][stash_len]
   int64_t stash_len;
+  uint8_t* q_frags; // or the query operands of attend_tiles, [batch][kv head][16 rows][D / 32 + 1] KB
+  float* q_units;   // and what their products are multiplied by, per row
+  int64_t q_tiles;  // 16-row tiles per sequence and head
   int64_t max_len;
   int chunk;        // slots of a split
   int nsplit, tiles, tile_rows;
@@ -251,14 +256,20 @@ struct Ring {
 
 // Copy a block to LDS (byte offset `to`, the same in all lanes): every load
 // instruction moves 1 KB, lane l's 16 bytes to `to` + 16 l.
-template <uint32_t BB>
+// STREAM: read once, the non-temporal policy.
+template <uint32_t BB, bool STREAM = true>
 __device__ __forceinline__ void copy_block(const uint8_t* from, uint32_t to, int lane) {
   const uint8_t* mine = from + lane * 16;
 #pragma unroll
   for (uint32_t i = 0; i < BB; i += 1024) {
-    if (BB - i >= 1024 || uint32_t(lane) * 16 < BB - i)
-      asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off nt"
-                   : : "v"(mine + i), "s"(to + i) : "memory", "m0");
+    if (BB - i >= 1024 || uint32_t(lane) * 16 < BB - i) {
+      if (STREAM)
+        asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off nt"
+                     : : "v"(mine + i), "s"(to + i) : "memory", "m0");
+      else
+        asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+                     : : "v"(mine + i), "s"(to + i) : "memory", "m0");
+    }
   }
 }
 template <int N>
@@ -1022,6 +1033,377 @@ __global__ void __launch_bounds__(256) finish_kernel(const AttnParams p, unsigne
   else weigh_stash(p, blockIdx.x - joins, lds);
 }
 
+// ------------------------------------------------ many rows per kv head ----
+// Prompts and chunks of them.  A workgroup holds 128 rows (64 at 256 channels),
+// 32 per wave, and walks over 64 slots at a time: the four waves unpack a quarter each of the
+// tile into LDS, in operand order, so that a fragment is 1 KB read and written
+// in lane order without conflicts; every fragment serves 32 rows of each wave.
+//   K  goes in as its codes (u / 256, exact), and s meets the 32-bit sums of its
+//      group; sum lo (sum of q) is a product of its own, of the lo of all groups
+//      with the sums of q, split in two fp16.  (With lo + s u rounded to fp16 in
+//      one fragment the scores lose more than an fp16 result shows: relative
+//      error 4.4e-4 instead of 2.9e-4 at 12001 slots, where its own rounding
+//      makes 2.1e-4.)
+//   V  goes in as lo + s u, rounded to fp16 once; so do the probabilities.
+// The codes of the next tile are loaded while this one is computed, and unpacked
+// into the other buffer after it: one barrier per tile.  The row sums are a
+// matrix product with ones, of the probabilities as rounded.
+constexpr int kTileSlots = 64;
+// 16-row tiles of a wave (two hold too many registers at 256 channels), rows of a workgroup
+constexpr int big_tiles(int D) { return D == 256 ? 1 : 2; }
+constexpr int big_rows(int D) { return 64 * big_tiles(D); }
+constexpr float kTileLift = 14.0f;   // p <= 2^14 in fp16; lost only below 2^-38 of the largest
+
+template <int D, int G>
+struct TileRegs {
+  static constexpr int NK = D / 32, NV = D / 16, CK = kchunk(D), VH = NV / 2, VG = NV / G, GH = (VH + VG - 1) / VG;
+  static constexpr int CV = VH < vchunk(D) ? VH : vchunk(D);
+  typename Chunk<CK>::type k[NK / CK];   // unit `wave` of the tile
+  uint32_t kp[G];
+  typename Chunk<CV>::type v[VH / CV];   // half `wave & 1` of the channels of block `wave >> 1`
+  u4_t vs[GH], vl[GH];
+
+  __device__ __forceinline__ void load(const uint8_t* base, int lane, int wave) {
+    const int u = wave & 1, half = wave & 1, g0 = half * VH / VG;
+#pragma unroll
+    for (int g = 0; g < G; g++) kp[g] = *reinterpret_cast<const uint32_t*>(base + kpair_at(G, 16 * u + (lane & 15), g));
+#pragma unroll
+    for (int i = 0; i < NK / CK; i++)
+      k[i] = *reinterpret_cast<const typename Chunk<CK>::type*>(base + kcode_at(D, G, u, lane, i * CK));
+#pragma unroll
+    for (int g = 0; g < GH; g++) {
+      const uint8_t* at = base + vstep_at(G, lane >> 4, 0, g0 + g);
+      vs[g] = *reinterpret_cast<const u4_t*>(at);
+      vl[g] = *reinterpret_cast<const u4_t*>(at + 16);
+    }
+#pragma unroll
+    for (int i = 0; i < VH / CV; i++)
+      v[i] = *reinterpret_cast<const typename Chunk<CV>::type*>(base + vcode_at(D, G, lane, half * VH + i * CV));
+  }
+  // Pairs of slots from `left` on (of the block) become 0, and with them the values.
+  __device__ __forceinline__ void cut(int left, int lane, int wave) {
+    if (16 * (wave & 1) + (lane & 15) >= left)
+#pragma unroll
+      for (int g = 0; g < G; g++) kp[g] = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+      if (vtoken(lane >> 4, e) >= left)
+#pragma unroll
+        for (int g = 0; g < GH; g++) {
+          const uint32_t keep = (e & 1) ? 0x0000ffffu : 0xffff0000u;
+          vs[g][e / 2] &= keep;
+          vl[g][e / 2] &= keep;
+        }
+  }
+  // kb, vb, lb: fragments; sb: s [unit][group][16 slots].
+  __device__ __forceinline__ void store(h8_t* kb, h8_t* vb, h8_t* lb, _Float16* sb, int lane, int wave) const {
+    const int blk = wave >> 1, half = wave & 1;
+#pragma unroll
+    for (int ks = 0; ks < NK; ks++) {
+      const uint32_t w = k[ks / CK][ks % CK];
+      h8_t f;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const h2_t x = code_pair_256th(w, i);
+        f[2 * i] = x[0];
+        f[2 * i + 1] = x[1];
+      }
+      kb[(wave * NK + ks) * 64 + lane] = f;
+    }
+    h8_t f;   // sets 0 and 1: lo of group e against the two parts of the sums of q
+#pragma unroll
+    for (int e = 0; e < 8; e++) f[e] = e < G && lane < 32 ? __builtin_bit_cast(h2_t, kp[e < G ? e : 0])[0] : (_Float16)0.0f;
+    lb[wave * 64 + lane] = f;
+    if (lane < 16)
+#pragma unroll
+      for (int g = 0; g < G; g++) sb[(wave * G + g) * 16 + lane] = __builtin_bit_cast(h2_t, kp[g])[1];
+#pragma unroll
+    for (int i = 0; i < VH; i++) {
+      const int c = half * VH + i;
+      u4_t vsg, vlg;
+      if constexpr (VH % VG == 0 || VG % VH == 0) {
+        vsg = vs[VH % VG == 0 ? i / VG : 0];
+        vlg = vl[VH % VG == 0 ? i / VG : 0];
+      } else {   // a group lies across the halves
+        const int g = c / VG - half * VH / VG;
+        vsg = vs[0];
+        vlg = vl[0];
+#pragma unroll
+        for (int x = 1; x < GH; x++)
+          if (g == x) { vsg = vs[x]; vlg = vl[x]; }
+      }
+      const uint32_t w = v[i / CV][i % CV];
+      h8_t f;
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const h2_t x = __builtin_elementwise_fma(code_pair(w, e), __builtin_bit_cast(h2_t, (uint32_t)vsg[e]),
+                                                 __builtin_bit_cast(h2_t, (uint32_t)vlg[e]));
+        f[2 * e] = x[0];
+        f[2 * e + 1] = x[1];
+      }
+      vb[(blk * NV + c) * 64 + lane] = f;
+    }
+  }
+};
+
+// The sums of q over its groups as an operand, divided by 256 and split in two
+// fp16: set 0 the rounded ones, set 1 what is left (e = group).
+template <int NK, int G>
+__device__ __forceinline__ h8_t sums_operand(const h8_t* qf, int set) {
+  constexpr int KG = NK / G;
+  h8_t r;
+#pragma unroll
+  for (int e = 0; e < 8; e++) {
+    r[e] = (_Float16)0.0f;
+    if (e < G) {
+      const float q = sum_sets(sum8<KG>(qf + (e < G ? e : 0) * KG)) * (1.0f / 256.0f);
+      const _Float16 hi = (_Float16)q;
+      r[e] = set == 0 ? hi : set == 1 ? (_Float16)(q - (float)hi) : (_Float16)0.0f;
+    }
+  }
+  return r;
+}
+// q . k / 256 of NT 16-row tiles and the tile's four units of 16 slots.
+template <int NT, int NK, int G>
+__device__ __forceinline__ void scores(const h8_t* kb, const h8_t* lb, const _Float16* sb, const h8_t (*qf)[NK],
+                                       const h8_t* qs, int lane, f4_t (*z)[4]) {
+  constexpr int KG = NK / G;
+  const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int u = 0; u < 4; u++) {
+    if (NK == 8) __builtin_amdgcn_sched_barrier(0);   // or the loads of all units are hoisted, and spilled
+    const h8_t lf = lb[u * 64 + lane];
+#pragma unroll
+    for (int t = 0; t < NT; t++) z[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lf, qs[t], zero, 0, 0, 0);
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+      f4_t a[NT];
+#pragma unroll
+      for (int t = 0; t < NT; t++) a[t] = zero;
+#pragma unroll
+      for (int ks = g * KG; ks < (g + 1) * KG; ks++) {
+        const h8_t kf = kb[(u * NK + ks) * 64 + lane];
+#pragma unroll
+        for (int t = 0; t < NT; t++) a[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[t][ks], a[t], 0, 0, 0);
+      }
+      const h4_t s = *reinterpret_cast<const h4_t*>(sb + (u * G + g) * 16 + 4 * (lane >> 4));
+#pragma unroll
+      for (int r = 0; r < 4; r++)
+#pragma unroll
+        for (int t = 0; t < NT; t++) z[t][u][r] = fmaf((float)s[r], a[t][r], z[t][u][r]);
+    }
+  }
+}
+
+// p from z, its sums, and p V.  EXACT: p as the sum of two fp16, for fp16
+// results: with V rounded as well, one alone makes their error 1.6 times that of
+// their own rounding (two: 1.4); bf16 results are eight times as coarse.
+template <bool EXACT, int NT, int NV>
+__device__ __forceinline__ void weigh_values(const f4_t (*z)[4], const float* z_unit, const float* ref, const h8_t* vb,
+                                             int lane, f4_t* sum, f4_t (*acc)[NV]) {
+  h8_t ones;
+#pragma unroll
+  for (int e = 0; e < 8; e++) ones[e] = (_Float16)1.0f;
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    h8_t pf[NT], rest[NT];
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const float x = exp2_fast(fmaf(z[t][2 * h + (e >> 2)][e & 3], z_unit[t], -ref[t]));
+        pf[t][e] = (_Float16)x;
+        if (EXACT) rest[t][e] = (_Float16)(x - (float)pf[t][e]);
+      }
+      sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pf[t], sum[t], 0, 0, 0);
+      if (EXACT) sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, rest[t], sum[t], 0, 0, 0);
+    }
+#pragma unroll
+    for (int c = 0; c < NV; c++) {
+      const h8_t vf = vb[(h * NV + c) * 64 + lane];
+#pragma unroll
+      for (int t = 0; t < NT; t++) {
+        acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[t], acc[t][c], 0, 0, 0);
+        if (EXACT) acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, rest[t], acc[t][c], 0, 0, 0);
+      }
+    }
+  }
+}
+
+template <int D, int G, bool EXACT>
+__global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attend_tiles(const AttnParams p) {
+  constexpr int NK = D / 32, NV = D / 16, NT = big_tiles(D);
+  __shared__ h8_t kbuf[2][4 * NK * 64], vbuf[2][2 * NV * 64], lbuf[2][4 * 64];
+  __shared__ __attribute__((aligned(16))) _Float16 sbuf[2][4 * G * 16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, set = lane >> 4;
+  // heads change fastest, so that an XCD's L2 keeps to few of them; the tiles
+  // that see most come first
+  const int hk = blockIdx.x, b = blockIdx.z;
+  const int tile = p.tiles - 1 - int(blockIdx.y / unsigned(p.nsplit)), split = int(blockIdx.y % unsigned(p.nsplit));
+  Span s;
+  seq_span(p, b, s);
+  const int row0 = tile * big_rows(D);
+  if (row0 >= s.rows) {
+    if (p.zero_rest && p.nsplit == 1) zero_rows<D>(p, b, hk, row0, min(row0 + big_rows(D), p.rows));
+    return;
+  }
+  tile_span(p, row0, s);
+  if (split >= used_splits(p, s) && split > 0) return;   // split 0 leaves its operands, and zeros if it is the only one
+  const int begin = int(s.lo) + split * p.chunk, end = int(min(int64_t(begin) + p.chunk, s.hi));
+  const int ntile = end > begin ? (end - begin + kTileSlots - 1) / kTileSlots : 0;
+
+  const int wrow = row0 + wave * 16 * NT;
+  h8_t qf[NT][NK], qs[NT];
+  float z_unit[NT], ref[NT], top[NT];
+  int from[NT], to[NT];
+  f4_t acc[NT][NV], sum[NT];
+#pragma unroll
+  for (int t = 0; t < NT; t++) {
+    const int row = wrow + t * 16 + n;
+    const bool there = row < s.rows;
+    float unit;
+    load_q<D>(p, b, hk, row, there, qf[t], &unit);
+    z_unit[t] = fabsf(p.scale2) * 256.0f * unit;
+    if (p.scale2 < 0.0f)   // the sign goes to q, so that the largest product is the largest z
+#pragma unroll
+      for (int ks = 0; ks < NK; ks++) qf[t][ks] = -qf[t][ks];
+    qs[t] = sums_operand<NK, G>(qf[t], set);
+    if (p.q_frags && split == 0) {   // for the weights
+      const int64_t rt = (int64_t(b) * p.c.heads + hk) * p.q_tiles + (wrow + t * 16) / 16;
+      h8_t* to = reinterpret_cast<h8_t*>(p.q_frags) + rt * (NK + 1) * 64 + lane;
+#pragma unroll
+      for (int ks = 0; ks < NK; ks++) to[ks * 64] = qf[t][ks];
+      to[NK * 64] = qs[t];
+      if (set == 0) p.q_units[rt * 16 + n] = z_unit[t];
+    }
+    int64_t f = 0, e = 0;
+    if (there) row_span(p, s, row, f, e);
+    from[t] = int(f);
+    to[t] = int(e);
+    ref[t] = top[t] = kNone;
+    sum[t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < NV; c++) acc[t][c] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  // what some row of the wave sees, and what all of them see
+  int any_from = 0, any_to = 0, all_from = 0, all_to = 0;
+  if (wrow < s.rows) {
+    int64_t f0, t0, f1, t1;
+    row_span(p, s, wrow, f0, t0);
+    row_span(p, s, min(wrow + 16 * NT, s.rows) - 1, f1, t1);
+    any_from = int(f0); any_to = int(t1); all_from = int(f1); all_to = int(t0);
+  }
+
+  int page[2];   // of the two blocks of tile (64 k + lane)
+  const int mask = (1 << p.c.shift) - 1;
+  auto pages = [&](int i0) {
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const int slot = begin + (i0 + lane) * kTileSlots + h * kBlock;
+      page[h] = -1;
+      if (i0 + lane < ntile && (slot >> p.c.shift) < p.c.width)
+        page[h] = p.c.table[int64_t(b) * p.c.table_stride + (slot >> p.c.shift)];
+      if (page[h] >= p.c.pages) page[h] = -1;
+    }
+  };
+  TileRegs<D, G> regs;
+  bool gone[2][2];   // by buffer and block
+  auto load = [&](int i) {
+    if ((i & 63) == 0) pages(i);
+    const int pg0 = __builtin_amdgcn_readlane(page[0], i & 63), pg1 = __builtin_amdgcn_readlane(page[1], i & 63);
+    gone[1][0] = pg0 < 0;
+    gone[1][1] = pg1 < 0;
+    const int pg = wave < 2 ? pg0 : pg1, slot = begin + i * kTileSlots + (wave >> 1) * kBlock;
+    // a block without a page is read from page 0 and cut away
+    regs.load(p.c.buf + uint64_t(max(pg, 0)) * p.c.page_bytes + uint64_t(hk) * p.c.head_bytes +
+                  uint32_t((slot & mask) / kBlock) * block_bytes(D, G), lane, wave);
+    const int left = pg < 0 ? 0 : int(s.len) - slot;
+    if (left < kBlock) regs.cut(left, lane, wave);
+  };
+  if (ntile > 0) {
+    load(0);
+    regs.store(kbuf[0], vbuf[0], lbuf[0], sbuf[0], lane, wave);
+  }
+
+#pragma unroll 1
+  for (int i = 0; i < ntile; i++) {
+    gone[0][0] = gone[1][0];
+    gone[0][1] = gone[1][1];
+    __syncthreads();
+    if (i + 1 < ntile) load(i + 1);
+    const int slot0 = begin + i * kTileSlots;
+    if (slot0 < any_to && slot0 + kTileSlots > any_from) {
+      const h8_t* kb = kbuf[i & 1];
+      const h8_t* vb = vbuf[i & 1];
+      f4_t z[NT][4];
+      scores<NT, NK, G>(kb, lbuf[i & 1], sbuf[i & 1], qf, qs, lane, z);
+      if (slot0 < all_from || slot0 + kTileSlots > all_to || gone[0][0] || gone[0][1]) {
+#pragma unroll
+        for (int t = 0; t < NT; t++)
+#pragma unroll
+          for (int u = 0; u < 4; u++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+              const int slot = slot0 + 16 * u + 4 * set + r;
+              z[t][u][r] = slot >= from[t] && slot < to[t] && !gone[0][u >> 1] ? z[t][u][r] : -__builtin_inff();
+            }
+      }
+      float mx[NT];
+      bool moves = false;
+#pragma unroll
+      for (int t = 0; t < NT; t++) {
+        float m = z[t][0][0];
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+#pragma unroll
+          for (int r = 0; r < 4; r++) m = fmaxf(m, z[t][u][r]);
+        mx[t] = m * z_unit[t];
+        moves |= mx[t] > top[t];
+      }
+      if (__any(moves)) {
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+          top[t] = fmaxf(top[t], max_sets(mx[t]));
+          const float r = top[t] - kTileLift, f = exp2_fast(ref[t] - r);
+          ref[t] = r;
+          sum[t] *= f;
+#pragma unroll
+          for (int c = 0; c < NV; c++) acc[t][c] *= f;
+        }
+      }
+      weigh_values<EXACT, NT, NV>(z, z_unit, ref, vb, lane, sum, acc);
+    }
+    if (i + 1 < ntile) {
+      const int o = (i + 1) & 1;
+      regs.store(kbuf[o], vbuf[o], lbuf[o], sbuf[o], lane, wave);
+    }
+  }
+
+#pragma unroll
+  for (int t = 0; t < NT; t++) {
+    const int row = wrow + t * 16 + n;
+    if (row >= s.rows) {
+      if (p.zero_rest && p.nsplit == 1 && row < p.rows)
+#pragma unroll
+        for (int c = 0; c < NV; c++)
+          *reinterpret_cast<u2_t*>(out_row(p, b, hk, row) + 16 * c + 4 * set) = u2_t{0u, 0u};
+      continue;
+    }
+    const float l = sum[t][0];
+    if (p.nsplit == 1) {
+#pragma unroll
+      for (int c = 0; c < NV; c++) put_out(p, b, hk, row, 16 * c + 4 * set, acc[t][c], l);
+      if (p.lse && set == 0) put_lse(p, b, hk, row, ref[t], l);
+    } else if (ntile > 0) {
+      const int64_t at = part_row(p, b, hk, split, row);
+#pragma unroll
+      for (int c = 0; c < NV; c++) *reinterpret_cast<f4_t*>(p.part + at * D + 16 * c + 4 * set) = acc[t][c];
+      if (set == 0) { p.part_rl[at * 2] = ref[t]; p.part_rl[at * 2 + 1] = l; }
+    }
+  }
+}
+
 // Weight of every cached slot: the sum of P over the sequence's rows, from the
 // rows' log-sum-exp.  A wave owns one block of 32 slots, so no two waves add to
 // one slot and the order of the sums is fixed.
@@ -1107,12 +1489,177 @@ __global__ void __launch_bounds__(256) weigh_kernel(const AttnParams p) {
   }
 }
 
+// Weights after attend_tiles, which leaves its query operands behind.  A wave
+// holds 64 slots of K in registers and goes through the rows that may see them,
+// 16 at a time; the operands come through LDS, 32 rows ahead by direct loads
+// shared by the four waves.  Per 16 rows and 64 slots: 20 matrix instructions
+// and about 130 others (16 of them exponentials), so vector work bounds it, at
+// about half of what attend_tiles takes for the same scores.
+template <int D, int G>
+__global__ void __launch_bounds__(256, D == 256 ? 1 : 2) weigh_tiles(const AttnParams p) {
+  constexpr int NK = D / 32, KG = NK / G, CK = kchunk(D), FR = NK + 1;   // 1 KB fragments of 16 rows
+  constexpr int kStage = 2;                                              // row tiles per stage
+  __shared__ h8_t qbuf[2][kStage * FR * 64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, set = lane >> 4;
+  const int hk = blockIdx.x, b = blockIdx.z;
+  Span s;
+  seq_span(p, b, s);
+  const int group0 = int(blockIdx.y) * 4 * kTileSlots, slot0 = group0 + wave * kTileSlots;
+  if (group0 >= s.len || s.rows == 0) return;
+  // tokens [t0, t1) of the queries see some slot of the workgroup
+  const int behind = int(s.len) - s.ql;
+  const int t0 = p.causal ? max(group0 - behind, 0) : 0;
+  const int t1 = p.window > 0 ? int(min(int64_t(group0) + 4 * kTileSlots - 1 + p.window - behind, int64_t(s.ql))) : s.ql;
+  if (t0 >= t1) return;
+  const int rt0 = t0 * int(p.gq) / 16, rt1 = (t1 * int(p.gq) + 15) / 16;
+
+  const int64_t item = int64_t(b) * p.c.heads + hk;
+  const h8_t* frags = reinterpret_cast<const h8_t*>(p.q_frags) + item * p.q_tiles * FR * 64;
+  const uint32_t to = uint32_t(uintptr_t((__attribute__((address_space(3))) void*)&qbuf[0][0]));
+  auto fetch = [&](int i) {   // stage i: every wave copies every fourth KB
+#pragma unroll
+    for (int k = 0; k < (kStage * FR + 3) / 4; k++) {
+      const int f = wave + k * 4;
+      if (f < kStage * FR && rt0 + i * kStage + f / FR < p.q_tiles)
+        copy_block<1024, false>(reinterpret_cast<const uint8_t*>(frags + (int64_t(rt0 + i * kStage) * FR + f) * 64),
+                         to + uint32_t(i & 1) * uint32_t(sizeof(qbuf[0])) + uint32_t(f) * 1024u, lane);
+    }
+  };
+  const int stages = (rt1 - rt0 + kStage - 1) / kStage;
+  fetch(0);
+
+  h8_t kf[4][NK], lf[4];
+  h4_t ks4[4][G];
+  bool gone[2];
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    const int first = slot0 + h * kBlock;
+    const uint8_t* base = first < s.len ? block_at<D, G>(p.c, b, hk, first) : nullptr;
+    gone[h] = base == nullptr;
+#pragma unroll
+    for (int v = 0; v < 2; v++) {
+      const int u = 2 * h + v;
+      uint32_t lo[G];
+#pragma unroll
+      for (int g = 0; g < G; g++) {
+        u4_t kp = {0u, 0u, 0u, 0u};
+        lo[g] = 0u;
+        if (base) {
+          kp = *reinterpret_cast<const u4_t*>(base + kpair_at(G, 16 * v + 4 * set, g));
+          lo[g] = *reinterpret_cast<const uint32_t*>(base + kpair_at(G, 16 * v + n, g));
+        }
+#pragma unroll
+        for (int r = 0; r < 4; r++) ks4[u][g][r] = __builtin_bit_cast(h2_t, (uint32_t)kp[r])[1];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e++)
+        lf[u][e] = e < G && lane < 32 ? __builtin_bit_cast(h2_t, lo[e < G ? e : 0])[0] : (_Float16)0.0f;
+#pragma unroll
+      for (int i = 0; i < NK / CK; i++) {
+        typename Chunk<CK>::type w = {};
+        if (base) w = *reinterpret_cast<const typename Chunk<CK>::type*>(base + kcode_at(D, G, v, lane, i * CK));
+#pragma unroll
+        for (int x = 0; x < CK; x++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const h2_t c = code_pair_256th(w[x], e);
+            kf[u][i * CK + x][2 * e] = c[0];
+            kf[u][i * CK + x][2 * e + 1] = c[1];
+          }
+      }
+    }
+  }
+  f4_t sum[4];
+#pragma unroll
+  for (int u = 0; u < 4; u++) sum[u] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const f4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  const float* lse = p.lse + int64_t(b) * p.q.tokens * p.q.heads;
+  const bool holes = gone[0] || gone[1] || slot0 + kTileSlots > s.len;
+
+#pragma unroll 1
+  for (int i = 0; i < stages; i++) {
+    wait_loads<0>();
+    __syncthreads();   // the stage is there, and the other buffer has been read
+    if (i + 1 < stages) fetch(i + 1);
+#pragma unroll
+    for (int k = 0; k < kStage; k++) {
+      const int rt = rt0 + i * kStage + k, row = rt * 16 + n;
+      if (rt >= rt1) continue;
+      int from = 0, to_ = 0;
+      float l2 = 0.0f, unit = 0.0f;
+      if (row < s.rows) {
+        int64_t f, t;
+        row_span(p, s, row, f, t);
+        from = int(f);
+        to_ = int(t);
+        const int tok = token_of(p, row);
+        l2 = lse[int64_t(tok) * p.q.heads + (hk - tok) * int(p.gq) + row] * kLog2e;
+        unit = p.q_units[item * p.q_tiles * 16 + row];
+      }
+      // rows of the tile: first .. last; what all of them see
+      int64_t f0, e0, f1, e1;
+      row_span(p, s, rt * 16, f0, e0);
+      row_span(p, s, min(rt * 16 + 16, s.rows) - 1, f1, e1);
+      if (e1 <= slot0 || f0 >= slot0 + kTileSlots) continue;
+      const bool whole = !holes && f1 <= slot0 && e0 >= slot0 + kTileSlots && rt * 16 + 16 <= s.rows;
+      const h8_t* qb = &qbuf[i & 1][k * FR * 64];
+      h8_t qf[NK];
+#pragma unroll
+      for (int ks = 0; ks < NK; ks++) qf[ks] = qb[ks * 64 + lane];
+      const h8_t qs = qb[NK * 64 + lane];
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        f4_t z = __builtin_amdgcn_mfma_f32_16x16x32_f16(lf[u], qs, zero, 0, 0, 0);
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+          f4_t a = zero;
+#pragma unroll
+          for (int ks = g * KG; ks < (g + 1) * KG; ks++)
+            a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u][ks], qf[ks], a, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < 4; r++) z[r] = fmaf((float)ks4[u][g][r], a[r], z[r]);
+        }
+        if (whole) {
+#pragma unroll
+          for (int r = 0; r < 4; r++) sum[u][r] += exp2_fast(fmaf(z[r], unit, -l2));
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; r++) {
+            const int slot = slot0 + 16 * u + 4 * set + r;
+            const float w = exp2_fast(fmaf(z[r], unit, -l2));
+            sum[u][r] += slot >= from && slot < to_ && !gone[u >> 1] ? w : 0.0f;
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; u++)
+#pragma unroll
+    for (int r = 0; r < 4; r++)
+#pragma unroll
+      for (int d = 1; d < 16; d *= 2) sum[u][r] += __shfl_xor(sum[u][r], d);
+  if (n == 0) {
+    float* w = p.weights + b * p.wsb + hk * p.wsh;
+#pragma unroll
+    for (int u = 0; u < 4; u++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        const int slot = slot0 + 16 * u + 4 * set + r;
+        if (slot < s.len) w[slot] += sum[u][r];
+      }
+  }
+}
+
 // ------------------------------------------------------------- dispatch ----
 struct Plan {
-  int nq, tile_rows, tiles, chunk, nsplit, shared;   // nq 0: attend_few
+  enum { FEW, ROWS, TILES } kind;
+  int nq, tile_rows, tiles, chunk, nsplit, shared;
   bool stash;
   int64_t stash_len, groups, joins, weighs;
-  size_t part, rl, lse, z, where, total;   // offsets in the workspace, its size
+  int64_t q_tiles;
+  size_t part, rl, lse, z, where, frags, units, total;   // offsets in the workspace, its size
 };
 
 // Variants and splits by shape alone.
@@ -1130,8 +1677,9 @@ static bool plan(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv
   // attend_few: a set of 64 channels has to share its pair; step numbers are below 2^30
   const int64_t steps = (spanned(kFewRows) + 2 * kBlock - 1) / (2 * kBlock), cost = steps + kItemCost;
   const bool few = rows <= kFewRows && c->group >= 64 && heads * cost < (int64_t(1) << 30);
-  pl->nq = few ? 0 : rows > kRowTile && c->head_dim < 256 ? 2 : 1;
-  pl->tile_rows = few ? kFewRows : pl->nq * kRowTile;
+  pl->kind = few ? Plan::FEW : rows > kManyRows ? Plan::TILES : Plan::ROWS;
+  pl->nq = rows > kRowTile && c->head_dim < 256 ? 2 : 1;   // attend_rows
+  pl->tile_rows = few ? kFewRows : pl->kind == Plan::TILES ? big_rows(c->head_dim) : pl->nq * kRowTile;
   pl->tiles = int((rows + pl->tile_rows - 1) / pl->tile_rows);
   const int64_t base = heads * pl->tiles;
   pl->shared = 0;
@@ -1149,9 +1697,12 @@ static bool plan(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv
   } else {
     const int64_t blocks = (spanned(pl->tile_rows) + kBlock - 1) / kBlock;
     const int64_t wanted = base > 0 ? (kWantedGroups + base - 1) / base : 1;
+    const bool big = pl->kind == Plan::TILES;
+    const int64_t least = big ? kMinTileBlocks : kMinBlocks, unit = big ? 2 : waves;
     int64_t per = (blocks + wanted - 1) / wanted;
-    per = per < kMinBlocks ? kMinBlocks : per > 64 * waves ? 64 * waves : per;   // 64 blocks per wave at most
-    per = (per + waves - 1) / waves * waves;
+    per = per < least ? least : per;
+    if (!big && per > 64 * waves) per = 64 * waves;   // 64 blocks per wave at most
+    per = (per + unit - 1) / unit * unit;
     pl->chunk = int(per) * kBlock;
     pl->nsplit = int(blocks ? (blocks + per - 1) / per : 1);
     part_rows = size_t(heads) * pl->nsplit * size_t(rows);
@@ -1161,8 +1712,12 @@ static bool plan(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv
   pl->stash = a->weights && rows <= kStashRows;
   pl->stash_len = (all + kBlock - 1) / kBlock * kBlock;
   pl->joins = split ? heads * rows : 0;
-  pl->weighs = !a->weights ? 0 : pl->stash ? heads * ((all + 1023) / 1024) : heads * ((all + 4 * kBlock - 1) / (4 * kBlock));
-  if (q->batch > 65535 || int64_t(pl->tiles) * c->kv_heads > 65535) return false;   // y and z of the grid
+  pl->q_tiles = int64_t(pl->tiles) * pl->tile_rows / 16;
+  const int64_t slots = pl->stash ? 1024 : pl->kind == Plan::TILES ? 4 * kTileSlots : 4 * kBlock;   // of a workgroup
+  pl->weighs = !a->weights ? 0 : heads * ((all + slots - 1) / slots);
+  if (pl->weighs > 0 && pl->kind == Plan::TILES && (all + slots - 1) / slots > 65535) return false;
+  // y and z of the grid
+  if (q->batch > 65535 || int64_t(pl->tiles) * (pl->kind == Plan::TILES ? pl->nsplit : c->kv_heads) > 65535) return false;
   if (!launchable(pl->groups, 256) || !launchable(pl->joins + pl->weighs, 256)) return false;
   size_t o = 0;
   auto take = [&](bool used, size_t bytes) {
@@ -1175,6 +1730,9 @@ static bool plan(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv
   pl->lse = take(a->weights && !pl->stash && !a->lse, size_t(q->batch) * a->q.tokens * a->q.heads * 4);
   pl->z = take(pl->stash, size_t(heads) * rows * pl->stash_len * 4);
   pl->where = take(pl->shared > 0, size_t(heads) * sizeof(int2));
+  const bool frags = a->weights && pl->kind == Plan::TILES;
+  pl->frags = take(frags, size_t(heads) * pl->q_tiles * (c->head_dim / 32 + 1) * 1024);
+  pl->units = take(frags, size_t(heads) * pl->q_tiles * 16 * 4);
   pl->total = o;
   return true;
 }
@@ -1186,16 +1744,17 @@ struct LaunchAttention {
   template <int D, int G>
   int go() {
     const dim3 grid(unsigned(pl.nsplit), unsigned(pl.tiles * p.c.heads), unsigned(p.c.batch)), threads(Ring<D, G>::NW * 64);
-    if constexpr (D / G >= 64) {
+    if (pl.kind == Plan::TILES) {
+      const dim3 tiles(unsigned(p.c.heads), unsigned(pl.tiles * pl.nsplit), unsigned(p.c.batch));
+      if (p.q.dtype == STAGQ_F16) hipLaunchKernelGGL((attend_tiles<D, G, true>), tiles, dim3(256), 0, st, p);
+      else hipLaunchKernelGGL((attend_tiles<D, G, false>), tiles, dim3(256), 0, st, p);
+    } else if (pl.kind == Plan::FEW) {
       const dim3 shares = p.shared ? dim3(unsigned(p.shared)) : grid;
-      if (pl.nq == 0) hipLaunchKernelGGL((attend_few<D, G>), shares, dim3(few_waves(D) * 64), 0, st, p);
-    }
-    if (pl.nq == 0) {
-    } else if constexpr (D < 256) {
-      if (pl.nq == 2) hipLaunchKernelGGL((attend_rows<D, G, 2>), grid, threads, 0, st, p);
-      else hipLaunchKernelGGL((attend_rows<D, G, 1>), grid, threads, 0, st, p);
-    } else {
+      if constexpr (D / G >= 64) hipLaunchKernelGGL((attend_few<D, G>), shares, dim3(few_waves(D) * 64), 0, st, p);
+    } else if (pl.nq == 1) {
       hipLaunchKernelGGL((attend_rows<D, G, 1>), grid, threads, 0, st, p);
+    } else {
+      if constexpr (D < 256) hipLaunchKernelGGL((attend_rows<D, G, 2>), grid, threads, 0, st, p);
     }
     int s = launched();
     if (s != STAGQ_OK) return s;
@@ -1205,7 +1764,11 @@ struct LaunchAttention {
       s = launched();
       if (s != STAGQ_OK) return s;
     }
-    if (pl.weighs > 0 && !pl.stash) {
+    if (pl.weighs > 0 && pl.kind == Plan::TILES) {
+      const dim3 groups(unsigned(p.c.heads), unsigned((p.max_len + 4 * kTileSlots - 1) / (4 * kTileSlots)), unsigned(p.c.batch));
+      hipLaunchKernelGGL((weigh_tiles<D, G>), groups, dim3(256), 0, st, p);
+      s = launched();
+    } else if (pl.weighs > 0 && !pl.stash) {
       hipLaunchKernelGGL((weigh_kernel<D, G>), dim3((unsigned)pl.weighs), dim3(256), 0, st, p);
       s = launched();
     }
@@ -1215,7 +1778,7 @@ struct LaunchAttention {
 
 static int check_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_attn* a) {
   int st = check_cache(c);
-  if (st == STAGQ_OK) st = check_seqs(q);
+  if (st == STAGQ_OK) st = check_seqs(c, q);
   if (st != STAGQ_OK) return st;
   if (!a) return STAGQ_EINVAL;
   if (a->q.heads < 1 || a->q.heads % c->kv_heads) return STAGQ_ESHAPE;
@@ -1267,6 +1830,9 @@ int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
   p.part_rl = pl.nsplit > 1 || pl.shared > 0 || pl.stash ? reinterpret_cast<float*>(ws + pl.rl) : nullptr;
   p.stash = pl.stash ? reinterpret_cast<float*>(ws + pl.z) : nullptr;
   p.stash_len = pl.stash_len;
+  p.q_frags = a->weights && pl.kind == Plan::TILES ? ws + pl.frags : nullptr;
+  p.q_units = reinterpret_cast<float*>(ws + pl.units);
+  p.q_tiles = pl.q_tiles;
   p.zero_rest = a->zero_rest != 0;
   p.scale2 = a->scale * kLog2e;
   p.gq = unsigned(a->q.heads / c->kv_heads);

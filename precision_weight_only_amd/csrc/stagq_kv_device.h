@@ -78,6 +78,13 @@ __device__ __forceinline__ h2_t code_pair(uint32_t x, int i) {
   return __builtin_bit_cast(h2_t, w) - k;
 }
 
+// And divided by 256 (exact).
+__device__ __forceinline__ h2_t code_pair_256th(uint32_t x, int i) {
+  const uint32_t w = ((x >> (4 * i)) & 0x000f000fu) | 0x64006400u;
+  const h2_t m = {(_Float16)0.00390625f, (_Float16)0.00390625f}, k = {(_Float16)-4.0f, (_Float16)-4.0f};
+  return __builtin_elementwise_fma(__builtin_bit_cast(h2_t, w), m, k);
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Reductions over the four lanes n, n + 16, n + 32, n + 48.

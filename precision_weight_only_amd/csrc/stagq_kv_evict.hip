@@ -247,7 +247,7 @@ struct LaunchEvict {
 
 static int check_evict(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_evict_args* e) {
   int st = check_cache(c);
-  if (st == STAGQ_OK) st = check_seqs(q);
+  if (st == STAGQ_OK) st = check_seqs(c, q);
   if (st != STAGQ_OK) return st;
   if (!e || e->keep < 1 || e->sinks < 0 || e->recent < 0 || e->max_len < 0) return STAGQ_EINVAL;
   if (int64_t(e->sinks) + e->recent > e->keep) return STAGQ_EINVAL;
@@ -267,7 +267,6 @@ static int check_evict(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
   const int64_t blocks = (int64_t(e->keep) + kBlock - 1) / kBlock;
   const int64_t heads = int64_t(q->batch) * c->kv_heads;
   if (!launchable(heads * blocks, 256) || !launchable(heads, kSelectThreads)) return STAGQ_ESHAPE;
-  if (reach(c, q, e->max_len) > (int64_t(1) << 30)) return STAGQ_ESHAPE;
   return STAGQ_OK;
 }
 

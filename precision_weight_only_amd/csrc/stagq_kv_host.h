@@ -18,13 +18,13 @@ inline int check_cache(const stagq_kv_cache* c) {
   return STAGQ_OK;
 }
 
-inline int check_seqs(const stagq_kv_seqs* q) {
+inline int check_seqs(const stagq_kv_cache* c, const stagq_kv_seqs* q) {
   if (!q || q->batch < 0 || q->table_width < 0) return STAGQ_EINVAL;
   if (q->batch == 0) return STAGQ_OK;
   if (!q->lengths || (q->table_width > 0 && !q->table)) return STAGQ_EINVAL;
   if (misaligned(q->table, 4) || misaligned(q->lengths, 4)) return STAGQ_EALIGN;
   if (q->batch > 1 && q->table_stride < q->table_width) return STAGQ_EINVAL;
-  if (q->batch > (1 << 20) || q->table_width > (1 << 23)) return STAGQ_ESHAPE;
+  if (q->batch > (1 << 20) || int64_t(q->table_width) * c->page_tokens > (int64_t(1) << 30)) return STAGQ_ESHAPE;   // slots are 31-bit numbers
   return STAGQ_OK;
 }
 

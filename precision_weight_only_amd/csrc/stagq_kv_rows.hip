@@ -217,7 +217,7 @@ struct LaunchRead {
 static int check_rows(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_tensor* k,
                       const stagq_kv_tensor* v, const int32_t* counts, RowsParams* p) {
   int st = check_cache(c);
-  if (st == STAGQ_OK) st = check_seqs(q);
+  if (st == STAGQ_OK) st = check_seqs(c, q);
   if (st != STAGQ_OK) return st;
   if (!k || !v) return STAGQ_EINVAL;
   st = check_tensor(*k, c->kv_heads, true, q->batch);

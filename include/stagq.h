@@ -424,7 +424,7 @@ int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
  * tokens that stay move together in their order.
  *   weights      fp32 [batch, kv_heads, >= max_len]
  *   weights_out  receives the weights of the tokens that stay, then 0 up to
- *                max_len; may be weights itself
+ *                max_len; may be weights itself, with the same strides
  *   kept         int32 [batch, kv_heads, keep]: the slots that stay, ascending,
  *                then -1
  *   out_lengths  int32 [batch]: min(n, keep); may be the sequences' lengths

@@ -1,11 +1,19 @@
 // Eviction from the key/value cache in 4 bits by accumulated attention weight.
 //
-// select: one workgroup per sequence and kv head finds the weight of the
-// lightest token that stays (a radix select over the order-preserving bits, 8
-// at a time), then writes the slots that stay in order and gathers their
-// weights.  gather: one workgroup per block of 32 tokens that stay and kv head
-// moves their codes and pairs.  All counts are integers, so no result depends
-// on the order of the atomics.
+// The slots that stay: a radix select over the order-preserving bits of the
+// weights (11, 11 and 10 of them) finds the lightest that stays, and a count of
+// heavier and equal ones gives every slot its place.  Up to kSmall slots one
+// workgroup per sequence and kv head does it all (select_kernel).  Beyond, one
+// workgroup would take 72 to 111 us at 65536 slots (its compute unit reads the
+// weights five times and counts in one LDS), so the slots are cut into parts of
+// 4096: count_kernel counts the first digit per part, sort_kernel adds the counts
+// up, counts the heavier slots and sets aside those with the deciding digit,
+// settle_kernel (one workgroup again, over those few) finds the weight itself and
+// where every part's slots go, write_kernel writes them.  Many weights are
+// exactly 0 and would meet in one counter: they are counted by ballot.
+// gather: one workgroup per block of 32 tokens that stay and kv head moves their
+// codes, pairs and weights.  All counts are integers, so no result depends on
+// the order of the atomics.
 #include "stagq_kv_host.h"
 
 namespace stagq {
@@ -27,6 +35,8 @@ struct EvictParams {
   int keep, sinks, recent;
   int64_t max_len;
   int blocks;             // of 32 tokens that stay, per sequence
+  int parts;              // of 4096 slots; 0: one workgroup per sequence and head selects
+  uint8_t* parts_ws;
 };
 
 __device__ __forceinline__ int seq_len(const EvictParams& p, int b) {
@@ -41,98 +51,343 @@ __device__ __forceinline__ uint32_t order_of(float v) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParams p) {
-  constexpr int NW = kSelectThreads / 64;
-  __shared__ int hist[256];
-  __shared__ int found_bin, found_rest;
-  __shared__ int n_above[NW], n_equal[NW];
-  const int hk = int(blockIdx.x % unsigned(p.c.heads)), b = int(blockIdx.x / unsigned(p.c.heads));
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int n = seq_len(p, b), m = min(n, p.keep);
-  const float* w = p.w + b * p.wsb + hk * p.wsh;
-  int* kept = p.kept + (int64_t(b) * p.c.heads + hk) * p.keep;
-  if (n <= p.keep) {
-    for (int i = tid; i < p.keep; i += kSelectThreads) kept[i] = i < n ? i : -1;
-  } else {
-    // the middle [sinks, end) gives `want` tokens
-    const int end = n - p.recent, want = p.keep - p.sinks - p.recent;
-    uint32_t prefix = 0, mask = 0;
-    int rest = want;
-    if (want > 0) {
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int i = p.sinks + tid; i < end; i += kSelectThreads) {
-          const uint32_t k = order_of(w[i]);
-          if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
-        }
-        __syncthreads();
-        if (wave == 0) {   // bins from the highest: 4 per lane, lane 0 the top ones
-          int c[4], total = 0;
-          for (int i = 0; i < 4; i++) { c[i] = hist[255 - (lane * 4 + i)]; total += c[i]; }
-          int before = total;
-          for (int d = 1; d < 64; d *= 2) { const int o = __shfl_up(before, d); if (lane >= d) before += o; }
-          before -= total;
-          for (int i = 0; i < 4; i++) {
-            if (before < rest && before + c[i] >= rest) { found_bin = 255 - (lane * 4 + i); found_rest = rest - before; }
-            before += c[i];
-          }
-        }
-        __syncthreads();
-        prefix |= uint32_t(found_bin) << shift;
-        mask |= 255u << shift;
-        rest = found_rest;
-        __syncthreads();
-      }
-    }
-    // stays: the ends, those above prefix, and the first `rest` equal to it
-    const int per = (n + NW * 64 - 1) / (NW * 64) * 64;
-    const int from = min(wave * per, n), to = min(from + per, n);
-    auto look = [&](int i, bool& above, bool& equal) {
-      above = equal = false;
-      if (i >= to) return;
-      if (i < p.sinks || i >= end) { above = true; return; }
-      if (want == 0) return;
-      const uint32_t k = order_of(w[i]);
-      above = k > prefix;
-      equal = k == prefix;
-    };
-    int na = 0, ne = 0;
-    for (int i = from; i < to; i += 64) {
-      bool a, e;
-      look(i + lane, a, e);
-      na += __popcll(__ballot(a));
-      ne += __popcll(__ballot(e));
-    }
-    if (lane == 0) { n_above[wave] = na; n_equal[wave] = ne; }
+constexpr int kWaves = kSelectThreads / 64, kBins = 2048;
+constexpr uint32_t kZeroKey = 0x80000000u;
+// Keys below that of -inf: slots that stay anyway, and slots past the end.
+constexpr uint32_t kEnd = 1u, kPast = 0u;
+
+// One sequence and kv head.
+struct Item {
+  int n, m, end, want;   // tokens; that stay; the middle [sinks, end) gives `want`
+  const float* w;
+  int* kept;
+};
+__device__ __forceinline__ Item item_of(const EvictParams& p, int b, int hk) {
+  Item t;
+  t.n = seq_len(p, b);
+  t.m = min(t.n, p.keep);
+  t.end = t.n - p.recent;
+  t.want = p.keep - p.sinks - p.recent;
+  t.w = p.w + b * p.wsb + hk * p.wsh;
+  t.kept = p.kept + (int64_t(b) * p.c.heads + hk) * p.keep;
+  return t;
+}
+__device__ __forceinline__ uint32_t key_at(const EvictParams& p, const Item& t, int i) {
+  return i >= t.n ? kPast : i < p.sinks || i >= t.end ? kEnd : order_of(t.w[i]);
+}
+__device__ __forceinline__ int shift_of(int pass) { return pass == 0 ? 21 : pass == 1 ? 10 : 0; }
+__device__ __forceinline__ uint32_t digit_mask(int pass) { return pass == 2 ? 1023u : 2047u; }
+
+struct SelectLds {
+  int hist[kBins];
+  int wave_sum[kWaves];
+  int bin, rest;
+  int above[kWaves], equal[kWaves];
+};
+__device__ __forceinline__ void clear_hist(SelectLds& s) {
+  for (int i = threadIdx.x; i < kBins; i += kSelectThreads) s.hist[i] = 0;
+  __syncthreads();
+}
+// Counts 64 keys; returns those that are 0, for the caller to add in one go.
+__device__ __forceinline__ int count_key(SelectLds& s, uint32_t k, uint32_t prefix, uint32_t mask, int pass) {
+  const bool in = k > kEnd && (k & mask) == prefix, zero = in && k == kZeroKey;
+  if (in && !zero) atomicAdd(&s.hist[(k >> shift_of(pass)) & digit_mask(pass)], 1);
+  return __popcll(__ballot(zero));
+}
+__device__ __forceinline__ void count_zeros(SelectLds& s, int zeros, int pass) {
+  if ((threadIdx.x & 63) == 0 && zeros) atomicAdd(&s.hist[(kZeroKey >> shift_of(pass)) & digit_mask(pass)], zeros);
+}
+// c0 and c1: counts of the bins 2047 - 2 tid and the one below.  Finds the bin
+// in which the count from the highest reaches `rest`: s.bin, and in s.rest how
+// many of it stay.
+__device__ __forceinline__ void find_bin(SelectLds& s, int c0, int c1, int rest) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b0 = kBins - 1 - 2 * tid;
+  int upto = c0 + c1;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) { const int o = __shfl_up(upto, d); if (lane >= d) upto += o; }
+  if (lane == 63) s.wave_sum[wave] = upto;
+  __syncthreads();
+  for (int i = 0; i < wave; i++) upto += s.wave_sum[i];
+  const int before = upto - c0 - c1;
+  if (before < rest && before + c0 >= rest) { s.bin = b0; s.rest = rest - before; }
+  else if (before + c0 < rest && upto >= rest) { s.bin = b0 - 1; s.rest = rest - before - c0; }
+  __syncthreads();
+}
+
+// Places of 64 slots' keys: `above` and `equal` stay so far, of those equal to
+// prefix the first `rest`.
+__device__ __forceinline__ void place_key(const EvictParams& p, const Item& t, int slot, uint32_t k, uint32_t prefix, int rest,
+                                          int& above, int& equal) {
+  const uint64_t below = (uint64_t(1) << (threadIdx.x & 63)) - 1;
+  const bool a = k == kEnd || k > prefix, e = k == prefix;
+  const uint64_t ma = __ballot(a), me = __ballot(e);
+  const int eq_rank = equal + __popcll(me & below);
+  const int at = above + __popcll(ma & below) + min(eq_rank, rest);
+  if ((a || (e && eq_rank < rest)) && at < p.keep) t.kept[at] = slot;
+  above += __popcll(ma);
+  equal += __popcll(me);
+}
+// Per wave: how many of its keys are above prefix (or stay anyway), and equal.
+__device__ __forceinline__ void tally_key(uint32_t k, uint32_t prefix, int& above, int& equal) {
+  above += __popcll(__ballot(k == kEnd || k > prefix));
+  equal += __popcll(__ballot(k == prefix));
+}
+
+// In place: weights move to lower or equal places, in tiles: a tile is read
+// before it is written, and later tiles read past it.
+__device__ __forceinline__ void weights_in_place(const EvictParams& p, const Item& t, float* wo) {
+  for (int i0 = 0; i0 < t.m; i0 += kSelectThreads) {
+    const int i = i0 + threadIdx.x;
+    const float v = i < t.m ? t.w[t.kept[i]] : 0.0f;
     __syncthreads();
-    int above = 0, equal = 0;   // before this wave's part
-    for (int i = 0; i < wave; i++) { above += n_above[i]; equal += n_equal[i]; }
-    const uint64_t below = (uint64_t(1) << lane) - 1;
-    for (int i = from; i < to; i += 64) {
-      bool a, e;
-      look(i + lane, a, e);
-      const uint64_t ma = __ballot(a), me = __ballot(e);
-      const int eq_rank = equal + __popcll(me & below);
-      const int at = above + __popcll(ma & below) + min(eq_rank, rest);
-      if ((a || (e && eq_rank < rest)) && at < p.keep) kept[at] = i + lane;
-      above += __popcll(ma);
-      equal += __popcll(me);
+    if (i < t.m) wo[i] = v;
+  }
+  __syncthreads();
+  for (int64_t i = t.m + threadIdx.x; i < p.max_len; i += kSelectThreads) wo[i] = 0.0f;
+}
+
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParams p) {
+  __shared__ SelectLds s;
+  const int hk = int(blockIdx.x % unsigned(p.c.heads)), b = int(blockIdx.x / unsigned(p.c.heads));
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Item t = item_of(p, b, hk);
+  if (t.n <= p.keep) {
+    for (int i = tid; i < p.keep; i += kSelectThreads) t.kept[i] = i < t.n ? i : -1;
+  } else {
+    const int each = (t.n + kWaves * 64 - 1) / (kWaves * 64), from = wave * each * 64 + lane;
+    // (with nothing wanted of the middle: prefix above all keys but NaN, of which 0 stay)
+    uint32_t prefix = t.want > 0 ? 0u : 0xffffffffu, mask = 0;
+    int rest = t.want;
+    for (int pass = 0; pass < 3 && t.want > 0; pass++) {
+      clear_hist(s);
+      int zeros = 0;
+#pragma unroll 4
+      for (int e = 0; e < each; e++) zeros += count_key(s, key_at(p, t, from + e * 64), prefix, mask, pass);
+      count_zeros(s, zeros, pass);
+      __syncthreads();
+      find_bin(s, s.hist[kBins - 1 - 2 * tid], s.hist[kBins - 2 - 2 * tid], rest);
+      prefix |= uint32_t(s.bin) << shift_of(pass);
+      mask |= digit_mask(pass) << shift_of(pass);
+      rest = s.rest;
     }
+    int above = 0, equal = 0;
+#pragma unroll 4
+    for (int e = 0; e < each; e++) tally_key(key_at(p, t, from + e * 64), prefix, above, equal);
+    if (lane == 0) { s.above[wave] = above; s.equal[wave] = equal; }
+    __syncthreads();
+    above = equal = 0;
+    for (int i = 0; i < wave; i++) { above += s.above[i]; equal += s.equal[i]; }
+#pragma unroll 4
+    for (int e = 0; e < each; e++)
+      place_key(p, t, from + e * 64, key_at(p, t, from + e * 64), prefix, rest, above, equal);
+  }
+  if (p.wout != p.w) return;   // else the gather kernel moves the weights
+  __threadfence_block();
+  __syncthreads();
+  weights_in_place(p, t, p.wout + b * p.osb + hk * p.osh);
+}
+
+// ------------------------------------------------------- many slots: parts ----
+constexpr int kPart = 4 * kSelectThreads;   // slots of a part, four per thread
+constexpr int kSmall = 2 * kPart;           // up to here select_kernel
+
+// Workspace of one item: [parts][2048] counts of the first digit, [parts][4096]
+// keys with the deciding one, [parts] PartInfo, and the Verdict.
+struct PartInfo {
+  int aside, above, equal, spare;   // keys set aside; then (settle) where the part's slots begin
+};
+struct Verdict {
+  uint32_t prefix;
+  int rest;
+};
+struct PartsWs {
+  int* hist;
+  uint32_t* keys;
+  PartInfo* info;
+  Verdict* verdict;
+};
+__host__ __device__ inline size_t parts_bytes(int parts) {   // of one item
+  return size_t(parts) * (kBins * 4 + kPart * 4 + sizeof(PartInfo)) + 256;
+}
+__device__ __forceinline__ PartsWs parts_ws(const EvictParams& p, int item) {
+  uint8_t* at = p.parts_ws + size_t(item) * parts_bytes(p.parts);
+  PartsWs r;
+  r.hist = reinterpret_cast<int*>(at);
+  r.keys = reinterpret_cast<uint32_t*>(r.hist + size_t(p.parts) * kBins);
+  r.info = reinterpret_cast<PartInfo*>(r.keys + size_t(p.parts) * kPart);
+  r.verdict = reinterpret_cast<Verdict*>(r.info + p.parts);
+  return r;
+}
+struct PartOf {
+  Item t;
+  PartsWs ws;
+  int part, parts, from;   // of the item's parts; first slot of the thread (then 64 further, four times)
+};
+__device__ __forceinline__ PartOf part_of(const EvictParams& p) {
+  const int item = blockIdx.y, b = item / p.c.heads;
+  PartOf r;
+  r.t = item_of(p, b, item - b * p.c.heads);
+  r.ws = parts_ws(p, item);
+  r.part = blockIdx.x;
+  r.parts = (r.t.n + kPart - 1) / kPart;
+  r.from = r.part * kPart + int(threadIdx.x >> 6) * 256 + int(threadIdx.x & 63);
+  return r;
+}
+
+__global__ void __launch_bounds__(kSelectThreads) count_kernel(const EvictParams p) {
+  __shared__ SelectLds s;
+  const PartOf o = part_of(p);
+  if (o.t.n <= p.keep || o.part >= o.parts || o.t.want == 0) return;
+  uint32_t k[4];
+#pragma unroll
+  for (int e = 0; e < 4; e++) k[e] = key_at(p, o.t, o.from + e * 64);
+  clear_hist(s);
+  int zeros = 0;
+#pragma unroll
+  for (int e = 0; e < 4; e++) zeros += count_key(s, k[e], 0u, 0u, 0);
+  count_zeros(s, zeros, 0);
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kSelectThreads) o.ws.hist[size_t(o.part) * kBins + i] = s.hist[i];
+}
+
+__global__ void __launch_bounds__(kSelectThreads) sort_kernel(const EvictParams p) {
+  __shared__ SelectLds s;
+  const PartOf o = part_of(p);
+  if (o.t.n <= p.keep || o.part >= o.parts || o.t.want == 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  uint32_t k[4];
+#pragma unroll
+  for (int e = 0; e < 4; e++) k[e] = key_at(p, o.t, o.from + e * 64);
+  int c0 = 0, c1 = 0;
+#pragma unroll 4
+  for (int i = 0; i < o.parts; i++) {
+    c0 += o.ws.hist[size_t(i) * kBins + kBins - 1 - 2 * tid];
+    c1 += o.ws.hist[size_t(i) * kBins + kBins - 2 - 2 * tid];
+  }
+  find_bin(s, c0, c1, o.t.want);
+  const uint32_t bin = uint32_t(s.bin);
+  int above = 0, aside = 0;
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    above += __popcll(__ballot(k[e] == kEnd || (k[e] > kEnd && (k[e] >> 21) > bin)));
+    aside += __popcll(__ballot(k[e] > kEnd && (k[e] >> 21) == bin));
+  }
+  if (lane == 0) { s.above[wave] = above; s.equal[wave] = aside; }
+  __syncthreads();
+  int at = 0, all = 0, sum = 0;
+  for (int i = 0; i < kWaves; i++) {
+    if (i < wave) at += s.equal[i];
+    all += s.equal[i];
+    sum += s.above[i];
+  }
+  uint32_t* keys = o.ws.keys + size_t(o.part) * kPart;
+  const uint64_t below = (uint64_t(1) << lane) - 1;
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    const bool in = k[e] > kEnd && (k[e] >> 21) == bin;
+    const uint64_t m = __ballot(in);
+    if (in) keys[at + __popcll(m & below)] = k[e];
+    at += __popcll(m);
+  }
+  if (tid == 0) {
+    o.ws.info[o.part] = PartInfo{all, sum, 0, 0};
+    if (o.part == 0) *o.ws.verdict = Verdict{bin << 21, s.rest};
+  }
+}
+
+__global__ void __launch_bounds__(kSelectThreads) settle_kernel(const EvictParams p) {
+  __shared__ SelectLds s;
+  const int item = blockIdx.x, b = item / p.c.heads;
+  const Item t = item_of(p, b, item - b * p.c.heads);
+  if (t.n <= p.keep || t.want == 0) return;
+  const PartsWs ws = parts_ws(p, item);
+  const int parts = (t.n + kPart - 1) / kPart;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  uint32_t prefix = ws.verdict->prefix, mask = 2047u << 21;
+  int rest = ws.verdict->rest;
+  for (int pass = 1; pass < 3; pass++) {
+    clear_hist(s);
+    int zeros = 0;
+    for (int i = wave; i < parts; i += kWaves) {   // a wave per part
+      const int n = ws.info[i].aside;
+      const uint32_t* keys = ws.keys + size_t(i) * kPart;
+#pragma unroll 4
+      for (int e = 0; e < n; e += 64) zeros += count_key(s, e + lane < n ? keys[e + lane] : kPast, prefix, mask, pass);
+    }
+    count_zeros(s, zeros, pass);
+    __syncthreads();
+    find_bin(s, s.hist[kBins - 1 - 2 * tid], s.hist[kBins - 2 - 2 * tid], rest);
+    prefix |= uint32_t(s.bin) << shift_of(pass);
+    mask |= digit_mask(pass) << shift_of(pass);
+    rest = s.rest;
+  }
+  for (int i = wave; i < parts; i += kWaves) {
+    const PartInfo in = ws.info[i];
+    const uint32_t* keys = ws.keys + size_t(i) * kPart;
+    int above = in.above, equal = 0;
+#pragma unroll 4
+    for (int e = 0; e < in.aside; e += 64) tally_key(e + lane < in.aside ? keys[e + lane] : kPast, prefix, above, equal);
+    if (lane == 0) ws.info[i] = PartInfo{in.aside, above, equal, 0};
   }
   __threadfence_block();
   __syncthreads();
-  // Weights move to lower or equal places, in tiles: a tile is read before it
-  // is written, and later tiles read past it.
-  float* wo = p.wout + b * p.osb + hk * p.osh;
-  for (int i0 = 0; i0 < m; i0 += kSelectThreads) {
-    const int i = i0 + tid;
-    const float v = i < m ? w[kept[i]] : 0.0f;
-    __syncthreads();
-    if (i < m) wo[i] = v;
+  if (wave == 0) {   // where the parts begin
+    int above = 0, equal = 0;
+    for (int i0 = 0; i0 < parts; i0 += 64) {
+      PartInfo in = {0, 0, 0, 0};
+      if (i0 + lane < parts) in = ws.info[i0 + lane];
+      int a = in.above, e = in.equal;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int x = __shfl_up(a, d), y = __shfl_up(e, d);
+        if (lane >= d) { a += x; e += y; }
+      }
+      if (i0 + lane < parts) ws.info[i0 + lane] = PartInfo{in.aside, above + a - in.above, equal + e - in.equal, 0};
+      above += __shfl(a, 63);
+      equal += __shfl(e, 63);
+    }
+    if (lane == 0) *ws.verdict = Verdict{prefix, rest};
   }
+}
+
+__global__ void __launch_bounds__(kSelectThreads) write_kernel(const EvictParams p) {
+  __shared__ SelectLds s;
+  const PartOf o = part_of(p);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (o.t.n <= p.keep) {   // all stay; the last part also writes what is past the slots
+    const int to = o.part == p.parts - 1 ? p.keep : min((o.part + 1) * kPart, p.keep);
+    for (int i = o.part * kPart + tid; i < to; i += kSelectThreads) o.t.kept[i] = i < o.t.n ? i : -1;
+    return;
+  }
+  if (o.part >= o.parts) return;
+  uint32_t k[4];
+#pragma unroll
+  for (int e = 0; e < 4; e++) k[e] = key_at(p, o.t, o.from + e * 64);
+  uint32_t prefix = 0xffffffffu;   // only the ends stay
+  int rest = 0, above = 0, equal = 0;
+  if (o.t.want > 0) {
+    const PartInfo in = o.ws.info[o.part];
+    prefix = o.ws.verdict->prefix;
+    rest = o.ws.verdict->rest;
+    above = in.above;
+    equal = in.equal;
+  } else {   // the ends before this part
+    const int at = o.part * kPart;
+    above = min(at, p.sinks) + max(at - o.t.end, 0);
+  }
+  int na = 0, ne = 0;
+#pragma unroll
+  for (int e = 0; e < 4; e++) tally_key(k[e], prefix, na, ne);
+  if (lane == 0) { s.above[wave] = na; s.equal[wave] = ne; }
   __syncthreads();
-  for (int64_t i = m + tid; i < p.max_len; i += kSelectThreads) wo[i] = 0.0f;
+  for (int i = 0; i < wave; i++) { above += s.above[i]; equal += s.equal[i]; }
+#pragma unroll
+  for (int e = 0; e < 4; e++) place_key(p, o.t, o.from + e * 64, k[e], prefix, rest, above, equal);
+}
+
+__global__ void __launch_bounds__(kSelectThreads) weights_kernel(const EvictParams p) {
+  const int item = blockIdx.x, b = item / p.c.heads, hk = item - b * p.c.heads;
+  weights_in_place(p, item_of(p, b, hk), p.wout + b * p.osb + hk * p.osh);
 }
 
 template <int D, int G>
@@ -157,6 +412,13 @@ __global__ void __launch_bounds__(256) gather_kernel(const EvictParams p) {
   const int hk = int(id % unsigned(p.c.heads)), b = int(id / unsigned(p.c.heads));
   const int m = min(seq_len(p, b), p.keep);
   if (blk == 0 && hk == 0 && threadIdx.x == 0) p.out_lengths[b] = m;
+  if (p.wout != p.w) {   // an equal part of the weights, each once
+    const int64_t part = (p.max_len + p.blocks - 1) / p.blocks, to = min((blk + 1) * part, p.max_len);
+    const float* w = p.w + b * p.wsb + hk * p.wsh;
+    const int* kept = p.kept + (int64_t(b) * p.c.heads + hk) * p.keep;
+    float* wo = p.wout + b * p.osb + hk * p.osh;
+    for (int64_t i = blk * part + threadIdx.x; i < to; i += 256) wo[i] = i < m ? w[kept[i]] : 0.0f;
+  }
   if (blk * kBlock >= m) return;
   uint8_t* dst = p.stage ? p.stage + ((int64_t(b) * p.c.heads + hk) * p.blocks + blk) * int64_t(block_bytes(D, G))
                          : out_block<D, G>(p, b, hk, blk);
@@ -234,7 +496,16 @@ struct LaunchEvict {
   template <int D, int G>
   int go() {
     const unsigned heads = unsigned(p.c.batch) * unsigned(p.c.heads);
-    hipLaunchKernelGGL(select_kernel, dim3(heads), dim3(kSelectThreads), 0, st, p);
+    if (p.parts == 0) {
+      hipLaunchKernelGGL(select_kernel, dim3(heads), dim3(kSelectThreads), 0, st, p);
+    } else {
+      const dim3 grid(unsigned(p.parts), heads), threads(kSelectThreads);
+      hipLaunchKernelGGL(count_kernel, grid, threads, 0, st, p);
+      hipLaunchKernelGGL(sort_kernel, grid, threads, 0, st, p);
+      hipLaunchKernelGGL(settle_kernel, dim3(heads), threads, 0, st, p);
+      hipLaunchKernelGGL(write_kernel, grid, threads, 0, st, p);
+      if (p.wout == p.w) hipLaunchKernelGGL(weights_kernel, dim3(heads), threads, 0, st, p);
+    }
     int s = launched();
     if (s != STAGQ_OK) return s;
     hipLaunchKernelGGL((gather_kernel<D, G>), dim3(heads * unsigned(p.blocks)), dim3(256), 0, st, p);
@@ -244,6 +515,8 @@ struct LaunchEvict {
     return launched();
   }
 };
+
+static int64_t parts_of(int64_t slots) { return slots <= kSmall ? 1 : (slots + kPart - 1) / kPart; }
 
 static int check_evict(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_evict_args* e) {
   int st = check_cache(c);
@@ -256,6 +529,9 @@ static int check_evict(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
   if (reach(c, q, e->max_len) > 0 && (!e->weights || !e->weights_out)) return STAGQ_EINVAL;
   if (e->weights_stride_seq < 0 || e->weights_stride_head < 0 || e->out_stride_seq < 0 || e->out_stride_head < 0)
     return STAGQ_EINVAL;
+  if (e->weights == e->weights_out &&
+      (e->weights_stride_seq != e->out_stride_seq || e->weights_stride_head != e->out_stride_head))
+    return STAGQ_EINVAL;
   if (misaligned(e->weights, 4) || misaligned(e->weights_out, 4) || misaligned(e->kept, 4) ||
       misaligned(e->out_lengths, 4) || misaligned(e->out_table, 4))
     return STAGQ_EALIGN;
@@ -266,7 +542,9 @@ static int check_evict(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
   }
   const int64_t blocks = (int64_t(e->keep) + kBlock - 1) / kBlock;
   const int64_t heads = int64_t(q->batch) * c->kv_heads;
-  if (!launchable(heads * blocks, 256) || !launchable(heads, kSelectThreads)) return STAGQ_ESHAPE;
+  if (!launchable(heads * blocks, 256) || !launchable(heads * parts_of(reach(c, q, e->max_len)), kSelectThreads) ||
+      heads > 65535)
+    return STAGQ_ESHAPE;
   return STAGQ_OK;
 }
 
@@ -274,6 +552,17 @@ static int check_evict(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
 static int evict_blocks(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_evict_args* e) {
   const int64_t r = reach(c, q, e->max_len), m = e->keep < r ? e->keep : r;
   return int(m > 0 ? (m + kBlock - 1) / kBlock : 1);
+}
+
+// Workspace: the staged blocks of an eviction in place, then that of the parts.
+static size_t stage_bytes(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_evict_args* e) {
+  if (e->out_table) return 0;
+  const size_t n = size_t(q->batch) * c->kv_heads * size_t(evict_blocks(c, q, e)) * block_bytes(c->head_dim, c->head_dim / c->group);
+  return (n + 255) / 256 * 256;
+}
+static size_t select_bytes(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_evict_args* e) {
+  const int64_t r = reach(c, q, e->max_len);
+  return r <= kSmall ? 0 : size_t(q->batch) * c->kv_heads * parts_bytes(int(parts_of(r)));
 }
 
 }  // namespace kv
@@ -284,8 +573,8 @@ using namespace stagq::kv;
 extern "C" {
 
 size_t stagq_kv_evict_workspace(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_evict_args* e) {
-  if (check_evict(c, q, e) != STAGQ_OK || e->out_table) return 0;
-  return size_t(q->batch) * c->kv_heads * size_t(evict_blocks(c, q, e)) * block_bytes(c->head_dim, c->head_dim / c->group);
+  if (check_evict(c, q, e) != STAGQ_OK) return 0;
+  return stage_bytes(c, q, e) + select_bytes(c, q, e);
 }
 
 int stagq_kv_evict(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv_evict_args* e, void* workspace,
@@ -316,6 +605,8 @@ int stagq_kv_evict(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_
   p.recent = e->recent;
   p.max_len = reach(c, q, e->max_len);
   p.blocks = evict_blocks(c, q, e);
+  p.parts = p.max_len <= kSmall ? 0 : int(parts_of(p.max_len));
+  p.parts_ws = static_cast<uint8_t*>(workspace) + stage_bytes(c, q, e);
   return by_shape(c, LaunchEvict{p, static_cast<hipStream_t>(hip_stream)});
 }
 

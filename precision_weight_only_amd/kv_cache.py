@@ -329,7 +329,7 @@ class KVCache:
                 out_lengths = torch.empty(B, dtype=_I32, device=self.device)
             e = _EVICT.pack(w, o, wb, wh, ob, oh, kept.data_ptr(), self._vector("evict", "out_lengths", out_lengths, B),
                             ot, os_, ow, keep, sinks, recent, reach, 0)
-            need = 0 if ot else self._lib.stagq_kv_evict_workspace(self._c, seqs, e)
+            need = self._lib.stagq_kv_evict_workspace(self._c, seqs, e)
             ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
             check(self._lib.stagq_kv_evict(self._c, seqs, e, ws.data_ptr() if need else 0, need, st), "stagq_kv_evict")
             return kept, out_lengths

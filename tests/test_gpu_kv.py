@@ -393,6 +393,9 @@ EVICT = [
     (64, 32, 32, [100, 33, 0, 5], 33, 4, 10), (128, 64, 64, [1500, 700], 400, 0, 0), (128, 64, 64, [2500], 1, 0, 0),
     (128, 128, 64, [200, 90], 64, 4, 60), (96, 32, 128, [300], 299, 0, 299), (256, 64, 32, [130, 131], 65, 65, 0),
     (256, 32, 256, [600], 128, 1, 3), (64, 64, 64, [5000], 1100, 3, 200),
+    # more slots than one workgroup selects from
+    (64, 64, 64, [8500, 0, 30, 12289], 5000, 4, 300), (64, 64, 256, [20000, 9000], 9500, 0, 0), (64, 64, 64, [9000], 40, 30, 10),
+    (64, 64, 64, [8300], 10000, 1, 1),
 ]
 
 
@@ -424,17 +427,18 @@ def test_evict(pwo, D, g, P, lens, keep, sinks, recent, inplace):
     check_evict(c, w, keep, sinks, recent, kept, lengths, wout, read)
 
 
-def test_evict_nan_infinity_and_all_equal(pwo):
-    _say("evict extremes")
+@pytest.mark.parametrize("n", [400, 9000])
+def test_evict_nan_infinity_and_all_equal(pwo, n):
+    _say("evict extremes", n)
     torch = _torch()
-    c = Case(pwo, [400], 1, 64, 64, 32, seed=2).fill()
-    for w in (np.zeros(416), np.full(416, np.inf), np.where(np.arange(416) % 7 == 0, np.nan, 1.0),
-              np.where(np.arange(416) % 5 == 0, -np.inf, 0.0)):
+    c = Case(pwo, [n], 1, 64, 64, 32, seed=2).fill()
+    i = np.arange(c.table.shape[1] * 32)
+    for w in (0.0 * i, np.full(i.shape, np.inf), np.where(i % 7 == 0, np.nan, 1.0), np.where(i % 5 == 0, -np.inf, 0.0)):
         w = w.astype(np.float32)[None, None]
         wt = torch.from_numpy(w.copy()).cuda()
         kept, _ = c.cache.evict(c.table, c.lengths, wt, 100, sinks=2, recent=9, weights_out=torch.empty_like(wt),
                                 out_table=torch.full((1, 4), -1, dtype=torch.int32, device="cuda"))   # no page: nothing moves
-        assert np.array_equal(kept[0, 0].cpu().numpy(), kv_oracle.evict(w[0, 0, :400], 100, 2, 9))
+        assert np.array_equal(kept[0, 0].cpu().numpy(), kv_oracle.evict(w[0, 0, :n], 100, 2, 9))
 
 
 # ------------------------------------------------------- together, captured ----

@@ -250,7 +250,7 @@ def test_attention_workspace_is_checked():
     (dict(keep=0), EINVAL), (dict(sinks=-1), EINVAL), (dict(recent=-1), EINVAL), (dict(sinks=6, recent=5), EINVAL),
     (dict(max_len=-2), EINVAL), (dict(weights=None), EINVAL), (dict(weights_out=None), EINVAL), (dict(kept=None), EINVAL),
     (dict(out_lengths=None), EINVAL), (dict(kept=4097), EALIGN), (dict(weights=4098), EALIGN),
-    (dict(out_stride_head=-1), EINVAL), (dict(out_table_stride=3), EINVAL), (dict(keep=200, out_table_width=3), ESIZE)])
+    (dict(out_stride_head=-1), EINVAL), (dict(out_stride_head=128), EINVAL), (dict(out_table_stride=3), EINVAL), (dict(keep=200, out_table_width=3), ESIZE)])
 def test_refused_eviction(bad, status):
     e = _evict(**bad)
     assert pwo.lib().stagq_kv_evict(A(_cache()), A(_seqs()), A(e), None, 0, None) == status
@@ -265,6 +265,10 @@ def test_eviction_in_place_needs_its_workspace():
     assert lib.stagq_kv_evict(A(c), A(s), A(e), 4096 + 8, need, None) == EALIGN
     assert lib.stagq_kv_evict(A(c), A(s), A(e), 4096, need - 1, None) == ESIZE
     assert lib.stagq_kv_evict_workspace(A(c), A(s), A(_evict())) == 0
+    # many slots are selected from in parts, with a workspace of their own
+    wide = _seqs(table_width=1000, table_stride=1000)
+    assert lib.stagq_kv_evict_workspace(A(c), A(wide), A(_evict())) > 0
+    assert lib.stagq_kv_evict(A(c), A(wide), A(_evict()), None, 1 << 30, None) == EINVAL
 
 
 def test_null_structs_and_empty_calls():

@@ -20,7 +20,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNone = -1e30f;  // reference of a row that has seen nothing
 constexpr int kRowTile = 16;
 constexpr int kWantedGroups = 512;  // two workgroups per CU
-constexpr int kMinBlocks = 16;      // of a split
+constexpr int kMinBlocks = 8;       // of a split
 constexpr int kMinTileBlocks = 16;  // of a split of attend_tiles
 constexpr int kManyRows = 32;       // beyond, attend_tiles
 constexpr int kOwnSteps = 16;       // attend_few: up to this many steps an item has one workgroup of its own
@@ -175,12 +175,6 @@ __device__ __forceinline__ void load_q(const AttnParams& p, int b, int hk, int r
     *unit = 1.0f / m;
   }
 }
-
-template <int N>
-struct Chunk;
-template <> struct Chunk<2> { typedef u2_t type; };
-template <> struct Chunk<3> { struct type { uint32_t v[3]; __device__ uint32_t operator[](int i) const { return v[i]; } }; };
-template <> struct Chunk<4> { typedef u4_t type; };
 
 // The waves' sums of a tile of ROWS rows meet in LDS: [wave][row][D + 4] floats,
 // then the references and sums of p, [wave][row] each.

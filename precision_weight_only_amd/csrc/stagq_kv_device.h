@@ -15,6 +15,13 @@ typedef float f4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
 
+// A lane's chunk of N code dwords (12-byte ones are 4-byte aligned).
+template <int N>
+struct Chunk;
+template <> struct Chunk<2> { typedef u2_t type; };
+template <> struct Chunk<3> { struct type { uint32_t v[3]; __device__ uint32_t operator[](int i) const { return v[i]; } }; };
+template <> struct Chunk<4> { typedef u4_t type; };
+
 // One strided tensor [batch, tokens, heads, head_dim].
 struct Tensor {
   uint8_t* data;

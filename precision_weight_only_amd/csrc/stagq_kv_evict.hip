@@ -52,6 +52,8 @@ __device__ __forceinline__ uint32_t order_of(float v) {
 }
 
 constexpr int kWaves = kSelectThreads / 64, kBins = 2048;
+constexpr int kPart = 4 * kSelectThreads;   // slots of a part, four per thread
+constexpr int kSmall = 2 * kPart;           // up to here select_kernel
 constexpr uint32_t kZeroKey = 0x80000000u;
 // Keys below that of -inf: slots that stay anyway, and slots past the end.
 constexpr uint32_t kEnd = 1u, kPast = 0u;
@@ -154,15 +156,19 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
   if (t.n <= p.keep) {
     for (int i = tid; i < p.keep; i += kSelectThreads) t.kept[i] = i < t.n ? i : -1;
   } else {
-    const int each = (t.n + kWaves * 64 - 1) / (kWaves * 64), from = wave * each * 64 + lane;
+    const int each = (t.n + kWaves * 64 - 1) / (kWaves * 64), from = wave * each * 64 + lane;   // each <= 8
+    uint32_t key[kSmall / kSelectThreads];
+#pragma unroll
+    for (int e = 0; e < kSmall / kSelectThreads; e++) key[e] = e < each ? key_at(p, t, from + e * 64) : kPast;
     // (with nothing wanted of the middle: prefix above all keys but NaN, of which 0 stay)
     uint32_t prefix = t.want > 0 ? 0u : 0xffffffffu, mask = 0;
     int rest = t.want;
     for (int pass = 0; pass < 3 && t.want > 0; pass++) {
       clear_hist(s);
       int zeros = 0;
-#pragma unroll 4
-      for (int e = 0; e < each; e++) zeros += count_key(s, key_at(p, t, from + e * 64), prefix, mask, pass);
+#pragma unroll
+      for (int e = 0; e < kSmall / kSelectThreads; e++)
+        if (e < each) zeros += count_key(s, key[e], prefix, mask, pass);
       count_zeros(s, zeros, pass);
       __syncthreads();
       find_bin(s, s.hist[kBins - 1 - 2 * tid], s.hist[kBins - 2 - 2 * tid], rest);
@@ -171,15 +177,15 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
       rest = s.rest;
     }
     int above = 0, equal = 0;
-#pragma unroll 4
-    for (int e = 0; e < each; e++) tally_key(key_at(p, t, from + e * 64), prefix, above, equal);
+#pragma unroll
+    for (int e = 0; e < kSmall / kSelectThreads; e++) tally_key(key[e], prefix, above, equal);
     if (lane == 0) { s.above[wave] = above; s.equal[wave] = equal; }
     __syncthreads();
     above = equal = 0;
     for (int i = 0; i < wave; i++) { above += s.above[i]; equal += s.equal[i]; }
-#pragma unroll 4
-    for (int e = 0; e < each; e++)
-      place_key(p, t, from + e * 64, key_at(p, t, from + e * 64), prefix, rest, above, equal);
+#pragma unroll
+    for (int e = 0; e < kSmall / kSelectThreads; e++)
+      if (e < each) place_key(p, t, from + e * 64, key[e], prefix, rest, above, equal);
   }
   if (p.wout != p.w) return;   // else the gather kernel moves the weights
   __threadfence_block();
@@ -188,9 +194,6 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
 }
 
 // ------------------------------------------------------- many slots: parts ----
-constexpr int kPart = 4 * kSelectThreads;   // slots of a part, four per thread
-constexpr int kSmall = 2 * kPart;           // up to here select_kernel
-
 // Workspace of one item: [parts][2048] counts of the first digit, [parts][4096]
 // keys with the deciding one, [parts] PartInfo, and the Verdict.
 struct PartInfo {
@@ -402,9 +405,12 @@ __device__ __forceinline__ uint8_t* out_block(const EvictParams& p, int b, int h
          uint32_t((slot & ((int64_t(1) << p.c.shift) - 1)) / kBlock) * block_bytes(D, G);
 }
 
+__device__ __forceinline__ void or_word(Chunk<3>::type& w, int k, uint32_t v) { w.v[k] |= v; }
+__device__ __forceinline__ void or_word(u4_t& w, int k, uint32_t v) { w[k] |= v; }
+
 template <int D, int G>
 __global__ void __launch_bounds__(256) gather_kernel(const EvictParams p) {
-  constexpr int NK = D / 32, NV = D / 16;
+  constexpr int NK = D / 32, NV = D / 16, CK = kchunk(D), CV = vchunk(D);
   __shared__ const uint8_t* src[kBlock];
   __shared__ int tok[kBlock];
   unsigned id = blockIdx.x;
@@ -436,13 +442,42 @@ __global__ void __launch_bounds__(256) gather_kernel(const EvictParams p) {
     tok[threadIdx.x] = t;
   }
   __syncthreads();
-  // K: every dword belongs to one token.
-  for (int it = threadIdx.x; it < 2 * 64 * NK; it += 256) {
-    const int ks = it % NK, lane = (it / NK) & 63, u = it / (64 * NK), t = u * 16 + (lane & 15);
-    const uint8_t* s = src[t];
-    uint32_t w = 0;
-    if (s) w = *reinterpret_cast<const uint32_t*>(s + kcode_at(D, G, tok[t] >> 4, (lane & 48) | (tok[t] & 15), ks));
-    *reinterpret_cast<uint32_t*>(dst + kcode_at(D, G, u, lane, ks)) = w;
+  // Codes, a lane's chunk of up to 16 bytes at a time.  K: a chunk belongs to one
+  // token.  V: every dword takes one nibble from each of its eight tokens.  A
+  // token without a page is read from the block's first (and gives 0), so that
+  // all loads are under way together.
+  constexpr int KI = 2 * 64 * (NK / CK), VI = 64 * (NV / CV);
+  typedef typename Chunk<CK>::type KW;
+  typedef typename Chunk<CV>::type VW;
+  const uint8_t* any = nullptr;
+  for (int t = 0; t < kBlock && !any; t++) any = src[t];
+  if (any) {
+    for (int it = threadIdx.x; it < KI; it += 256) {
+      const int lane = it & 63, c = (it >> 6) % (NK / CK), u = (it >> 6) / (NK / CK), t = u * 16 + (lane & 15);
+      const uint8_t* s = src[t];
+      KW w = *reinterpret_cast<const KW*>((s ? s : any) + kcode_at(D, G, tok[t] >> 4, (lane & 48) | (tok[t] & 15), c * CK));
+      if (!s) w = KW{};
+      *reinterpret_cast<KW*>(dst + kcode_at(D, G, u, lane, c * CK)) = w;
+    }
+    for (int it = threadIdx.x; it < VI; it += 256) {
+      const int lane = it & 63, c = it >> 6, set = lane >> 4;
+      VW w = {};
+      VW x[8];
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const int t = vtoken(set, e);
+        const uint8_t* s = src[t];
+        x[e] = *reinterpret_cast<const VW*>((s ? s : any) + vcode_at(D, G, vset(tok[t]) * 16 + (lane & 15), c * CV));
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const int t = vtoken(set, e), from = 4 * nibble(velem(tok[t]));
+        const uint32_t keep = src[t] ? 15u : 0u;
+#pragma unroll
+        for (int k = 0; k < CV; k++) or_word(w, k, ((x[e][k] >> from) & keep) << (4 * nibble(e)));
+      }
+      *reinterpret_cast<VW*>(dst + vcode_at(D, G, lane, c * CV)) = w;
+    }
   }
   for (int it = threadIdx.x; it < kBlock * G; it += 256) {
     const int t = it % kBlock, g = it / kBlock;
@@ -459,20 +494,6 @@ __global__ void __launch_bounds__(256) gather_kernel(const EvictParams p) {
     uint8_t* v = dst + vstep_at(G, vset(t), velem(t), g);
     *reinterpret_cast<uint16_t*>(v) = vs;
     *reinterpret_cast<uint16_t*>(v + 16) = vl;
-  }
-  // V: a dword takes one nibble from each of its eight tokens.
-  for (int it = threadIdx.x; it < 64 * NV; it += 256) {
-    const int lane = it & 63, ct = it >> 6, set = lane >> 4;
-    uint32_t w = 0;
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      const int t = vtoken(set, e);
-      const uint8_t* s = src[t];
-      if (!s) continue;
-      const uint32_t x = *reinterpret_cast<const uint32_t*>(s + vcode_at(D, G, vset(tok[t]) * 16 + (lane & 15), ct));
-      w |= ((x >> (4 * nibble(velem(tok[t])))) & 15u) << (4 * nibble(e));
-    }
-    *reinterpret_cast<uint32_t*>(dst + vcode_at(D, G, lane, ct)) = w;
   }
 }
 

@@ -383,7 +383,7 @@ int stagq_kv_read(const stagq_kv_cache* c, const stagq_kv_seqs* q, const int32_t
  * Attention of query rows over the cache.  Row i < q_lens[b] (clamped to
  * 0..q.tokens; NULL: all) stands at position p = lengths[b] - q_lens[b] + i and
  * sees slot t if t < lengths[b], t <= p where causal, and t > p - window where
- * window > 0 (which needs causal).  q head h reads kv head
+ * window > 0 (which needs causal).  scale is any number up to 2^100 in size.  q head h reads kv head
  * h / (q.heads / kv_heads).  With P = softmax(scale q . k) over what it sees,
  * out = sum P v; a row that sees nothing gets 0.
  *   lse      NULL or fp32 [batch, q.tokens, q.heads]: ln sum exp(scale q . k)
@@ -395,7 +395,8 @@ int stagq_kv_read(const stagq_kv_cache* c, const stagq_kv_seqs* q, const int32_t
  *            a longer sequence is cut to it
  *   zero_rest  not 0: rows of out from q_lens[b] on are set to 0
  * Rows of q from q_lens[b] on do not matter; those of lse and (without zero_rest)
- * out are left as they were.  q and out are fp16 or bf16, both the same.
+ * out are left as they were.  q and out are fp16 or bf16, both the same, and do
+ * not overlap.  Sequences: up to 65535.
  */
 typedef struct {
   stagq_kv_tensor q, out;
@@ -428,7 +429,8 @@ int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
  *   kept         int32 [batch, kv_heads, keep]: the slots that stay, ascending,
  *                then -1
  *   out_lengths  int32 [batch]: min(n, keep); may be the sequences' lengths
- *   out_table    pages the tokens move to (none of them among the pages read),
+ *   out_table    pages the tokens move to (none of them among the pages read;
+ *                the sequences' own table is refused),
  *                or NULL: they move within their own pages
  * 0 <= sinks, recent; sinks + recent <= keep; keep >= 1.
  */

@@ -1262,6 +1262,11 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attend_tiles(const Attn
     if (p.scale2 < 0.0f)   // the sign goes to q, so that the largest product is the largest z
 #pragma unroll
       for (int ks = 0; ks < NK; ks++) qf[t][ks] = -qf[t][ks];
+    if (z_unit[t] < 0x1p-126f) {   // a scale of 0: z is 0 by q, as -inf, what is not seen, may not meet a factor of 0
+      z_unit[t] = 1.0f;
+#pragma unroll
+      for (int ks = 0; ks < NK; ks++) qf[t][ks] = h8_t{};
+    }
     qs[t] = sums_operand<NK, G>(qf[t], set);
     if (p.q_frags && split == 0) {   // for the weights
       const int64_t rt = (int64_t(b) * p.c.heads + hk) * p.q_tiles + (wrow + t * 16) / 16;
@@ -1780,8 +1785,9 @@ static int check_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, cons
   if (st == STAGQ_OK) st = check_tensor(a->out, a->q.heads, false, q->batch);
   if (st != STAGQ_OK) return st;
   if (a->q.dtype != a->out.dtype || a->q.tokens != a->out.tokens) return STAGQ_EINVAL;
+  if (a->out.data && a->out.data == a->q.data) return STAGQ_EINVAL;   // q is read until the end
   if (a->window < 0 || (a->window > 0 && !a->causal) || a->max_len < 0) return STAGQ_EINVAL;
-  if (!(a->scale - a->scale == 0.0f)) return STAGQ_EINVAL;   // infinite or NaN
+  if (!(fabsf(a->scale) <= 0x1p100f)) return STAGQ_EINVAL;   // NaN, infinite or so large that its products are
   if (misaligned(a->q_lens, 4) || misaligned(a->lse, 4) || misaligned(a->weights, 4)) return STAGQ_EALIGN;
   if (a->weights && (a->weights_stride_seq < 0 || a->weights_stride_head < 0)) return STAGQ_EINVAL;
   return STAGQ_OK;

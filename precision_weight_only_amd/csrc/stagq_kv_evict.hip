@@ -262,10 +262,11 @@ __global__ void __launch_bounds__(kSelectThreads) sort_kernel(const EvictParams 
 #pragma unroll
   for (int e = 0; e < 4; e++) k[e] = key_at(p, o.t, o.from + e * 64);
   int c0 = 0, c1 = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < o.parts; i++) {
-    c0 += o.ws.hist[size_t(i) * kBins + kBins - 1 - 2 * tid];
-    c1 += o.ws.hist[size_t(i) * kBins + kBins - 2 - 2 * tid];
+    const int2 c = *reinterpret_cast<const int2*>(o.ws.hist + size_t(i) * kBins + kBins - 2 - 2 * tid);
+    c0 += c.y;
+    c1 += c.x;
   }
   find_bin(s, c0, c1, o.t.want);
   const uint32_t bin = uint32_t(s.bin);
@@ -557,15 +558,16 @@ static int check_evict(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
       misaligned(e->out_lengths, 4) || misaligned(e->out_table, 4))
     return STAGQ_EALIGN;
   if (e->out_table) {
+    if (e->out_table == q->table) return STAGQ_EINVAL;   // the same pages: NULL is the call for that
     if (e->out_table_width < 0 || (q->batch > 1 && e->out_table_stride < e->out_table_width)) return STAGQ_EINVAL;
     if (int64_t(e->out_table_width) * c->page_tokens < (e->keep < reach(c, q, e->max_len) ? e->keep : reach(c, q, e->max_len)))
       return STAGQ_ESIZE;
   }
   const int64_t blocks = (int64_t(e->keep) + kBlock - 1) / kBlock;
   const int64_t heads = int64_t(q->batch) * c->kv_heads;
-  if (!launchable(heads * blocks, 256) || !launchable(heads * parts_of(reach(c, q, e->max_len)), kSelectThreads) ||
-      heads > 65535)
-    return STAGQ_ESHAPE;
+  const int64_t parts = parts_of(reach(c, q, e->max_len));
+  if (!launchable(heads * blocks, 256) || !launchable(heads * parts, kSelectThreads)) return STAGQ_ESHAPE;
+  if (parts > 1 && heads > 65535) return STAGQ_ESHAPE;   // y of the grid
   return STAGQ_OK;
 }
 

@@ -120,12 +120,18 @@ def check_attention(case, q, out, q_lens=None, scale=None, causal=True, window=0
                 got, want = _np(lse)[b, :t, h * gq:(h + 1) * gq], r["lse"]
                 none = want == -np.inf
                 assert (got[none] == -np.inf).all()
-                assert (np.abs(got - want)[~none] <= (dz + 2.0 ** -21 * (1 + np.abs(want)))[~none]).all()
+                assert (np.abs(got[~none] - want[~none]) <= (dz + 2.0 ** -21 * (1 + np.abs(want)))[~none]).all()
             if weights is not None:
                 got = _np(weights)[b, h, :n] - 0.0
                 base = before[b, h, :n]
-                rows_dz = dz.max() if dz.size else 0.0
-                tol_w = np.expm1(2 * rows_dz) * r["weights"] + 2.0 ** -20 * (base + r["weights"]) + 1e-30
+                # A weight is exp(z - lse): what lse may be off by in 32 bits, the bound
+                # of it above, is an error of the exponent next to z's.  (Where z is
+                # exactly 0, scale 0, dz is 0 and this is all that is left: 150 slots,
+                # lse 5.01, one step of which is 4.8e-7 of the weight; log2, its
+                # product with ln 2 and back are three roundings of that size.)
+                seen = np.abs(r["lse"][np.isfinite(r["lse"])])
+                off = 2 * (dz.max() if dz.size else 0.0) + 2.0 ** -21 * (1 + (seen.max() if seen.size else 0.0))
+                tol_w = np.expm1(off) * r["weights"] + 2.0 ** -20 * (base + r["weights"]) + 1e-30
                 assert (np.abs(got - base - r["weights"]) <= tol_w).all()
     _say(f"worst {worst:.3f} of the bound")
 
@@ -262,6 +268,64 @@ def test_one_token(pwo, D, g, P, Hkv, gq, lens, dtype, window):
         assert np.array_equal(_np(w)[b, :, n:], before[b, :, n:])
     again = c.cache.attention(q, c.table, c.lengths, window=window, max_len=max(lens))
     check_attention(c, q, again, window=window)
+
+
+LONG = [
+    # rows of few heads, sequences long enough for the grid to share their steps
+    # D, g, P, Hkv, gq, T, lens, dtype, window
+    (128, 64, 64, 2, 4, 1, [2100, 0, 1, 1500], "float16", 0),
+    (128, 128, 32, 1, 2, 2, [3000, 40], "bfloat16", 0),
+    (64, 64, 256, 3, 1, 4, [1100, 1030, 64], "float16", 0),
+    (256, 128, 64, 1, 3, 1, [1500, 2], "float16", 0),
+    (256, 64, 32, 2, 1, 3, [1200], "bfloat16", 1100),
+    (128, 64, 64, 1, 4, 1, [5000, 300], "float16", 2000),
+    (64, 64, 32, 1, 1, 1, [70 * i % 1300 for i in range(70)], "float16", 0),          # more sequences than lanes
+    (128, 64, 64, 8, 1, 1, [1100] + [1] * 130, "bfloat16", 0),                         # most at their first token
+]
+
+
+@pytest.mark.parametrize("D,g,P,Hkv,gq,T,lens,dtype,window", LONG)
+def test_few_rows_of_long_sequences(pwo, D, g, P, Hkv, gq, T, lens, dtype, window):
+    _say("few rows, long", D, g, P, Hkv, gq, T, lens[:4], dtype, window)
+    torch = _torch()
+    c = Case(pwo, lens, Hkv, D, g, P, dtype=dtype, seed=14, extra_width=1).fill()
+    q = c.queries(T, Hkv * gq)
+    ql = [min(T, n) for n in lens]
+    lse = torch.full(q.shape[:3], 5.0, device="cuda")
+    w = torch.rand(len(lens), Hkv, c.table.shape[1] * P, device="cuda")
+    before = _np(w)
+    out = c.cache.attention(q, c.table, c.lengths, q_lens=torch.tensor(ql, dtype=torch.int32).cuda(), window=window, lse=lse,
+                            weights=w)
+    check_attention(c, q, out, q_lens=ql, window=window, lse=lse, weights=w, before=before)
+    for b, n in enumerate(lens):
+        assert (out[b, ql[b]:] == 0).all() and (lse[b, ql[b]:] == 5.0).all()
+        assert np.array_equal(_np(w)[b, :, n:], before[b, :, n:])
+
+
+@pytest.mark.parametrize("T", [1, 3, 40])
+@pytest.mark.parametrize("scale", [-0.09, 0.0])
+def test_other_scales(pwo, T, scale):
+    """A negative scale turns the order of the scores; 0 gives the mean of what is seen."""
+    _say("scale", T, scale)
+    torch = _torch()
+    c = Case(pwo, [150, 20], 1, 128, 64, 64, seed=15).fill()
+    q = c.queries(T, 4)
+    lse = torch.zeros(q.shape[:3], device="cuda")
+    w = torch.zeros(2, 1, c.table.shape[1] * 64, device="cuda")
+    out = c.cache.attention(q, c.table, c.lengths, scale=scale, lse=lse, weights=w)
+    check_attention(c, q, out, scale=scale, lse=lse, weights=w, before=np.zeros(w.shape))
+
+
+def test_split_chunk_of_a_long_sequence(pwo):
+    """Rows enough for the tiles, slots enough for their splits to be joined."""
+    _say("split chunk")
+    torch = _torch()
+    c = Case(pwo, [3000], 1, 128, 64, 64, seed=16).fill()
+    q = c.queries(12, 4)
+    lse = torch.zeros(q.shape[:3], device="cuda")
+    w = torch.zeros(1, 1, c.table.shape[1] * 64, device="cuda")
+    out = c.cache.attention(q, c.table, c.lengths, lse=lse, weights=w)
+    check_attention(c, q, out, lse=lse, weights=w, before=np.zeros(w.shape))
 
 
 MANY = [

@@ -151,7 +151,10 @@ def _tensor(**kw):
 
 def _attn(q=None, out=None, **kw):
     q = q or _tensor(heads=4, stride_token=512, stride_seq=1024)
-    f = dict(q=q, out=out or q, q_lens=None, lse=None, weights=None, weights_stride_seq=0, weights_stride_head=0,
+    if out is None:
+        out = type(q).from_buffer_copy(q)
+        out.data = 8192
+    f = dict(q=q, out=out, q_lens=None, lse=None, weights=None, weights_stride_seq=0, weights_stride_head=0,
              scale=0.1, causal=1, window=0, max_len=0, zero_rest=0, spare=0)
     f.update(kw)
     return KvAttn(**f)
@@ -159,7 +162,7 @@ def _attn(q=None, out=None, **kw):
 
 def _evict(**kw):
     f = dict(weights=4096, weights_out=4096, weights_stride_seq=512, weights_stride_head=256, out_stride_seq=512,
-             out_stride_head=256, kept=4096, out_lengths=4096, out_table=4096, out_table_stride=4, out_table_width=4,
+             out_stride_head=256, kept=4096, out_lengths=4096, out_table=8192, out_table_stride=4, out_table_width=4,
              keep=10, sinks=2, recent=3, max_len=0, spare=0)
     f.update(kw)
     return KvEvict(**f)
@@ -226,10 +229,10 @@ def test_refused_pairs_of_tensors():
 
 @pytest.mark.parametrize("bad,status", [
     (dict(window=-1), EINVAL), (dict(window=4, causal=0), EINVAL), (dict(max_len=-1), EINVAL),
-    (dict(scale=math.inf), EINVAL), (dict(scale=math.nan), EINVAL), (dict(lse=4098), EALIGN), (dict(q_lens=4097), EALIGN),
+    (dict(scale=math.inf), EINVAL), (dict(scale=-1e31), EINVAL), (dict(scale=math.nan), EINVAL), (dict(lse=4098), EALIGN), (dict(q_lens=4097), EALIGN),
     (dict(weights=4098), EALIGN), (dict(weights=4096, weights_stride_seq=-1), EINVAL),
     (dict(out=_tensor(heads=4, dtype=1)), EINVAL), (dict(out=_tensor(heads=4, tokens=5)), EINVAL),
-    (dict(q=_tensor(heads=5)), ESHAPE), (dict(q=_tensor(heads=4, dtype=2)), EINVAL)])
+    (dict(q=_tensor(heads=5)), ESHAPE), (dict(out=_tensor(heads=4, stride_token=512, stride_seq=1024)), EINVAL), (dict(q=_tensor(heads=4, dtype=2)), EINVAL)])
 def test_refused_attention(bad, status):
     a = _attn(**bad)
     assert pwo.lib().stagq_kv_attention(A(_cache()), A(_seqs()), A(a), None, 0, None) == status
@@ -250,7 +253,8 @@ def test_attention_workspace_is_checked():
     (dict(keep=0), EINVAL), (dict(sinks=-1), EINVAL), (dict(recent=-1), EINVAL), (dict(sinks=6, recent=5), EINVAL),
     (dict(max_len=-2), EINVAL), (dict(weights=None), EINVAL), (dict(weights_out=None), EINVAL), (dict(kept=None), EINVAL),
     (dict(out_lengths=None), EINVAL), (dict(kept=4097), EALIGN), (dict(weights=4098), EALIGN),
-    (dict(out_stride_head=-1), EINVAL), (dict(out_stride_head=128), EINVAL), (dict(out_table_stride=3), EINVAL), (dict(keep=200, out_table_width=3), ESIZE)])
+    (dict(out_stride_head=-1), EINVAL), (dict(out_stride_head=128), EINVAL), (dict(out_table_stride=3), EINVAL), (dict(keep=200, out_table_width=3), ESIZE),
+    (dict(out_table=4096), EINVAL)])
 def test_refused_eviction(bad, status):
     e = _evict(**bad)
     assert pwo.lib().stagq_kv_evict(A(_cache()), A(_seqs()), A(e), None, 0, None) == status

@@ -319,7 +319,9 @@ int stagq_unpack_host(const void* image, size_t image_bytes, stagq_info* shape, 
  * attention and reads touch; a call that writes must not write one slot twice.
  *
  * Every call checks its arguments on the host, is asynchronous on hip_stream,
- * allocates nothing and can be captured.  Results do not depend on timing
+ * allocates nothing and can be captured.  What a call writes must not overlap
+ * itself (strides of 0 or smaller than what they step over: STAGQ_EINVAL) nor
+ * what the call reads, unless said otherwise.  Results do not depend on timing
  * (fixed orders of summation, no floating-point atomics).
  */
 
@@ -429,9 +431,9 @@ int stagq_kv_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
  *   kept         int32 [batch, kv_heads, keep]: the slots that stay, ascending,
  *                then -1
  *   out_lengths  int32 [batch]: min(n, keep); may be the sequences' lengths
- *   out_table    pages the tokens move to (none of them among the pages read;
- *                the sequences' own table is refused),
- *                or NULL: they move within their own pages
+ *   out_table    pages the tokens move to (none of them among the pages read; the
+ *                sequences' own table is refused), or NULL: they move within
+ *                their own pages, which no two sequences may share then
  * 0 <= sinks, recent; sinks + recent <= keep; keep >= 1.
  */
 typedef struct {

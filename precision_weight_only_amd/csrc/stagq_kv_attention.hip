@@ -1790,6 +1790,9 @@ static int check_attention(const stagq_kv_cache* c, const stagq_kv_seqs* q, cons
   if (!(fabsf(a->scale) <= 0x1p100f)) return STAGQ_EINVAL;   // NaN, infinite or so large that its products are
   if (misaligned(a->q_lens, 4) || misaligned(a->lse, 4) || misaligned(a->weights, 4)) return STAGQ_EALIGN;
   if (a->weights && (a->weights_stride_seq < 0 || a->weights_stride_head < 0)) return STAGQ_EINVAL;
+  if (!disjoint(a->out, q->batch, c->head_dim)) return STAGQ_EINVAL;
+  if (a->weights && !disjoint(reach(c, q, a->max_len), q->batch, a->weights_stride_seq, c->kv_heads, a->weights_stride_head))
+    return STAGQ_EINVAL;
   return STAGQ_OK;
 }
 

@@ -551,6 +551,7 @@ static int check_evict(const stagq_kv_cache* c, const stagq_kv_seqs* q, const st
   if (reach(c, q, e->max_len) > 0 && (!e->weights || !e->weights_out)) return STAGQ_EINVAL;
   if (e->weights_stride_seq < 0 || e->weights_stride_head < 0 || e->out_stride_seq < 0 || e->out_stride_head < 0)
     return STAGQ_EINVAL;
+  if (!disjoint(reach(c, q, e->max_len), q->batch, e->out_stride_seq, c->kv_heads, e->out_stride_head)) return STAGQ_EINVAL;
   if (e->weights == e->weights_out &&
       (e->weights_stride_seq != e->out_stride_seq || e->weights_stride_head != e->out_stride_head))
     return STAGQ_EINVAL;

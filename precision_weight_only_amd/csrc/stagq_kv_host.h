@@ -39,6 +39,27 @@ inline int check_tensor(const stagq_kv_tensor& t, int heads, bool f32, int batch
   return STAGQ_OK;
 }
 
+// Whether an array that a call writes is free of overlaps with itself: rows of
+// `inner` adjacent elements, and the strides nested (each one covers what the
+// smaller ones span).
+inline bool disjoint(int64_t inner, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2 = 1, int64_t s2 = 0) {
+  int64_t n[3] = {n0, n1, n2}, s[3] = {s0, s1, s2}, extent = inner;
+  for (int done = 0; done < 3; done++) {
+    int at = -1;
+    for (int i = 0; i < 3; i++)
+      if (n[i] > 1 && (at < 0 || s[i] < s[at])) at = i;
+    if (at < 0) return true;
+    if (s[at] < extent) return false;
+    if (s[at] > INT64_MAX / 4 / n[at]) return false;
+    extent += s[at] * (n[at] - 1);
+    n[at] = 1;
+  }
+  return true;
+}
+inline bool disjoint(const stagq_kv_tensor& t, int batch, int head_dim) {
+  return disjoint(head_dim, batch, t.stride_seq, t.tokens, t.stride_token, t.heads, t.stride_head);
+}
+
 inline Cache make_cache(const stagq_kv_cache* c, const stagq_kv_seqs* q) {
   Cache r;
   r.buf = static_cast<uint8_t*>(c->buf);

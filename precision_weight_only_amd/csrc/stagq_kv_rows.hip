@@ -334,6 +334,7 @@ int stagq_kv_read(const stagq_kv_cache* c, const stagq_kv_seqs* q, const int32_t
   const int st = check_rows(c, q, k, v, start, &p);
   if (st != STAGQ_OK) return st;
   if (q->batch == 0 || p.blocks == 0) return STAGQ_OK;
+  if (k->data == v->data || !disjoint(*k, q->batch, c->head_dim) || !disjoint(*v, q->batch, c->head_dim)) return STAGQ_EINVAL;
   p.zero_rest = zero_rest;
   return by_shape(c, LaunchRead{p, static_cast<hipStream_t>(hip_stream)});
 }

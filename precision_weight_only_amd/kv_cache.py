@@ -81,6 +81,9 @@ class KVCache:
     buffer: a uint8 tensor to use (at least nbytes, 256-byte aligned); by default
     one is allocated, filled with 0.
 
+    The calls answer with values only: none of them records a gradient.  Tensors
+    that a call writes must not overlap themselves (an expanded one does).
+
     Every call runs on the given stream, or the device's current one, and
     returns without waiting for it.  Workspaces come from torch's allocator on
     that stream, one per call, so calls on several streams and captured ones do
@@ -249,6 +252,9 @@ class KVCache:
             raise ValueError(f"attention: {heads} heads of q over {self.kv_heads} kv heads")
         ql = self._vector("attention", "q_lens", q_lens, B)
         reach = self._reach("attention", W, max_len)
+        window = int(window)
+        if not 0 <= window < 2 ** 31:
+            raise ValueError(f"attention: window must be 0 (none) or a number of slots below 2^31, not {window}")
         ls = 0
         if lse is not None:
             if (not isinstance(lse, torch.Tensor) or lse.dtype != _F32 or lse.device != self.device
@@ -272,14 +278,15 @@ class KVCache:
                                           1 if causal else 0, window, reach, 1 if fresh and ql else 0, 0)
             key = (B, n, heads, window, reach, ls != 0, w != 0)
             need = self._needs.get(key)
-            if need is None:
+            first = need is None
+            if first:
                 need = self._lib.stagq_kv_attention_workspace(self._c, seqs, a)
-                if len(self._needs) < 4096:
-                    self._needs[key] = need
             ws = torch.empty(need, dtype=torch.uint8, device=self.device).data_ptr() if need else 0
             status = self._lib.stagq_kv_attention(self._c, seqs, a, ws, need, st)
             if status:
                 check(status, "stagq_kv_attention")
+            if first and len(self._needs) < 4096:   # not that of a refused call, which is 0
+                self._needs[key] = need
             return out
 
         return self._run(stream, call)

@@ -302,6 +302,58 @@ def test_few_rows_of_long_sequences(pwo, D, g, P, Hkv, gq, T, lens, dtype, windo
         assert np.array_equal(_np(w)[b, :, n:], before[b, :, n:])
 
 
+def test_a_refused_call_leaves_nothing_behind(pwo):
+    """The same call with an argument put right works (its workspace is not that of the refused one)."""
+    _say("refused, then right")
+    torch = _torch()
+    c = Case(pwo, [1500, 1300], 2, 128, 64, 64, seed=17).fill()
+    q = c.queries(1, 4)
+    for bad in (dict(scale=math.inf), dict(out=q), dict(window=5, causal=False)):
+        with pytest.raises(pwo.StagQError):
+            c.cache.attention(q, c.table, c.lengths, **bad)
+    with pytest.raises(ValueError):
+        c.cache.attention(q, c.table, c.lengths, window=-1)
+    with pytest.raises(pwo.StagQError):
+        c.cache.attention(q, c.table, c.lengths, out=torch.zeros_like(q[:1]).expand(2, -1, -1, -1))
+    check_attention(c, q, c.cache.attention(q, c.table, c.lengths))
+    check_attention(c, q, c.cache.attention(q, c.table, c.lengths, window=5), window=5)
+
+
+def test_no_pages(pwo):
+    """A table of width 0, and a cache of no pages."""
+    _say("no pages")
+    torch = _torch()
+    c = Case(pwo, [5, 0], 2, 64, 64, 32, seed=18)
+    kv = torch.zeros(2, 1, 2, 64, dtype=c.dt, device="cuda")
+    for cache, table in ((c.cache, c.table[:, :0]), (pwo.KVCache(0, 2, 64, page_tokens=32), c.table)):
+        for T in (1, 5, 40):
+            q = c.queries(T, 4)
+            lse = torch.zeros(q.shape[:3], device="cuda")
+            w = torch.ones(2, 2, table.shape[1] * 32, device="cuda")
+            cache.append(kv, kv, table, c.lengths)
+            out = cache.attention(q, table, c.lengths, lse=lse, weights=w)
+            assert (out == 0).all() and (lse == -math.inf).all() and (w == 1).all()
+        k, v = cache.read(table, c.lengths, tokens=3)
+        assert (k == 0).all() and (v == 0).all()
+    kept, n = c.cache.evict(c.table[:, :0], c.lengths, torch.ones(2, 2, 0, device="cuda"), keep=3)
+    assert (kept == -1).all() and (n == 0).all()
+
+
+def test_eviction_of_many_slots_into_its_own_lengths(pwo):
+    """out_lengths may be lengths itself, also where the selection takes several launches."""
+    _say("own lengths")
+    torch = _torch()
+    c = Case(pwo, [9000, 300, 8500], 1, 64, 64, 128, seed=19).fill()
+    w = torch.rand(3, 1, c.table.shape[1] * 128, device="cuda")
+    cache2 = pwo.KVCache(c.pages, 1, 64, page_tokens=128, buffer=c.cache.buffer.clone())
+    w2, l2 = w.clone(), c.lengths.clone()
+    kept, n = c.cache.evict(c.table, c.lengths, w, keep=400, sinks=4, recent=100)
+    kept2, n2 = cache2.evict(c.table, l2, w2, keep=400, sinks=4, recent=100, out_lengths=l2)
+    assert n2 is l2 and n.tolist() == [400, 300, 400] and torch.equal(n, l2)
+    assert torch.equal(kept, kept2) and torch.equal(w, w2)
+    assert all(torch.equal(a, b) for a, b in zip(c.cache.read(c.table, n), cache2.read(c.table, n)))
+
+
 @pytest.mark.parametrize("T", [1, 3, 40])
 @pytest.mark.parametrize("scale", [-0.09, 0.0])
 def test_other_scales(pwo, T, scale):
@@ -586,6 +638,99 @@ def test_captured_steps_replay(pwo):
     a, b = runs
     assert all(torch.equal(x, y) for x, y in zip(a[0], b[0]))
     assert torch.equal(a[1], b[1]) and torch.equal(a[2], b[2]) and torch.equal(a[3], b[3])
+
+
+@pytest.mark.parametrize("lens,keep", [([300, 41], 90), ([9000, 100], 500)])
+def test_captured_chunk_and_eviction_replay(pwo, lens, keep):
+    """A chunk appended, attended to with weights and evicted in place, with the lengths updated in place, captured in
+    one graph: every replay equals the eager calls, bit for bit."""
+    _say("captured chunk", lens)
+    torch = _torch()
+    c = Case(pwo, lens, 2, 64, 64, 64, seed=21, extra_width=1)
+    c.cache.buffer.zero_()
+    k, v, q, start = c.k[:, :40].clone(), c.v[:, :40].clone(), c.queries(40, 4), c.lengths.clone()
+    new = torch.tensor([40, 9], dtype=torch.int32).cuda()
+    w = torch.rand(2, 2, c.table.shape[1] * 64, device="cuda")
+    out, lse = torch.empty_like(q), torch.zeros(q.shape[:3], device="cuda")
+    kept = torch.empty(2, 2, keep, dtype=torch.int32, device="cuda")
+    c.fill()
+    state = [t.clone() for t in (c.cache.buffer, c.lengths, w)]
+
+    def step():
+        c.cache.append(k, v, c.table, c.lengths, new_lens=new)
+        c.cache.attention(q, c.table, c.lengths, q_lens=new, out=out, lse=lse, weights=w)
+        c.cache.evict(c.table, c.lengths, w, keep=keep, sinks=4, recent=16, kept=kept, out_lengths=c.lengths)
+
+    def reset(i):
+        for t, s in zip((c.cache.buffer, c.lengths, w), state):
+            t.copy_(s)
+        k.copy_(c.k[:, :40] * (0.5 + i))
+        q.mul_(1.01)
+
+    def results():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (c.cache.buffer, c.lengths, w, out, lse, kept)]
+
+    q0, runs, graph = q.clone(), [], None
+    for captured in (False, True):
+        q.copy_(q0), out.zero_(), lse.zero_(), reset(0)
+        if captured:
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                step()
+            torch.cuda.current_stream().wait_stream(side)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+            q.copy_(q0), out.zero_(), lse.zero_(), reset(0)
+        for i in range(4):
+            reset(i)
+            graph.replay() if captured else step()
+            runs.append(results())
+            _ = c.cache.attention(q, c.table, c.lengths)
+    for a, b in zip(runs[:4], runs[4:]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("T", [1, 6, 40])
+def test_a_row_that_is_not_finite_stays_alone(pwo, T):
+    """NaN or an infinity in a row of q: that row is NaN, the others are what they are without it."""
+    _say("NaN row", T)
+    torch = _torch()
+    c = Case(pwo, [200, 1200], 1, 128, 64, 64, seed=22).fill()
+    q = c.queries(T, 3)
+    clean = c.cache.attention(q, c.table, c.lengths)
+    bad = q.clone()
+    bad[0, 0, 1, 5] = math.nan
+    bad[1, T - 1, 2, 7] = math.inf
+    out = c.cache.attention(bad, c.table, c.lengths)
+    hit = torch.zeros(q.shape[:3], dtype=torch.bool, device="cuda")
+    hit[0, 0, 1] = hit[1, T - 1, 2] = True
+    assert out[hit].isnan().all()
+    # the reference that exponents are taken from may move at another slot: one more rounding of each p, and of out
+    assert (out[~hit].double() - clean[~hit].double()).abs().max() <= 2.0 ** -9 * float(clean.abs().max())
+
+
+def test_every_call_on_a_given_stream(pwo):
+    _say("given stream")
+    torch = _torch()
+    side = torch.cuda.Stream()
+    res = []
+    for stream in (None, side):
+        c = Case(pwo, [150, 70], 2, 64, 64, 32, seed=23)
+        c.cache.buffer.zero_()
+        w = torch.zeros(2, 2, c.table.shape[1] * 32, device="cuda")
+        q = c.queries(2, 4)
+        torch.cuda.synchronize()
+        c.cache.append(c.k, c.v, c.table, c.lengths, new_lens=c.lengths, stream=stream)
+        out = c.cache.attention(q, c.table, c.lengths, weights=w, stream=stream)
+        kept, n = c.cache.evict(c.table, c.lengths, w, keep=50, stream=stream)
+        k, v = c.cache.read(c.table, n, tokens=50, stream=stream)
+        side.synchronize()
+        torch.cuda.synchronize()
+        res.append((out, kept, n, k, v, w))
+    assert all(torch.equal(a, b) for a, b in zip(*res))
 
 
 def test_two_streams_at_once(pwo):

@@ -271,8 +271,33 @@ def test_eviction_in_place_needs_its_workspace():
     assert lib.stagq_kv_evict_workspace(A(c), A(s), A(_evict())) == 0
     # many slots are selected from in parts, with a workspace of their own
     wide = _seqs(table_width=1000, table_stride=1000)
-    assert lib.stagq_kv_evict_workspace(A(c), A(wide), A(_evict())) > 0
-    assert lib.stagq_kv_evict(A(c), A(wide), A(_evict()), None, 1 << 30, None) == EINVAL
+    e = _evict(weights_stride_seq=1 << 17, weights_stride_head=1 << 16, out_stride_seq=1 << 17, out_stride_head=1 << 16)
+    assert lib.stagq_kv_evict_workspace(A(c), A(wide), A(e)) > 0
+    assert lib.stagq_kv_evict(A(c), A(wide), A(e), None, 1 << 30, None) == EINVAL
+
+
+@pytest.mark.parametrize("bad", [dict(stride_seq=0), dict(stride_token=0), dict(stride_head=0), dict(stride_head=120),
+                                 dict(stride_token=128), dict(stride_seq=256), dict(stride_seq=1 << 62)])
+def test_what_is_written_may_not_overlap_itself(bad):
+    lib = pwo.lib()
+    c, s = _cache(), _seqs(batch=3)
+    f = dict(heads=4, stride_token=512, stride_seq=1024)
+    f.update(bad)
+    assert lib.stagq_kv_attention(A(c), A(s), A(_attn(out=_tensor(data=8192, **f))), None, 0, None) == EINVAL
+    t, far = _tensor(**bad), _tensor(data=1 << 30)
+    assert lib.stagq_kv_read(A(c), A(s), None, A(t), A(far), 0, None) == EINVAL
+    assert lib.stagq_kv_read(A(c), A(s), None, A(far), A(t), 0, None) == EINVAL
+    assert lib.stagq_kv_read(A(c), A(s), None, A(far), A(far), 0, None) == EINVAL
+
+
+@pytest.mark.parametrize("seq,head", [(0, 256), (512, 0), (512, 255), (511, 256), (256, 256)])
+def test_weights_written_may_not_overlap(seq, head):
+    lib = pwo.lib()
+    c, s = _cache(), _seqs(batch=3)   # 2 heads of up to 256 slots
+    assert lib.stagq_kv_attention(A(c), A(s), A(_attn(weights=1 << 20, weights_stride_seq=seq, weights_stride_head=head)),
+                                  None, 0, None) == EINVAL
+    e = _evict(weights_out=1 << 20, out_stride_seq=seq, out_stride_head=head)
+    assert lib.stagq_kv_evict(A(c), A(s), A(e), None, 0, None) == EINVAL
 
 
 def test_null_structs_and_empty_calls():

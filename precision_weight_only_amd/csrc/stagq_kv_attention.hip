@@ -21,10 +21,28 @@ constexpr float kNone = -1e30f;  // reference of a row that has seen nothing
 constexpr int kRowTile = 16;
 constexpr int kWantedGroups = 512;  // two workgroups per CU
 constexpr int kMinBlocks = 8;       // of a split
-constexpr int kMinTileBlocks = 16;  // of a split of attend_tiles
-constexpr int kManyRows = 32;       // beyond, attend_tiles
-constexpr int kOwnSteps = 16;       // attend_few: up to this many steps an item has one workgroup of its own
-constexpr int kStashRows = 8;       // up to this many rows z is kept for the weights
+// Rules of plan(), measured with 8 kv heads of 128 channels unless said otherwise.
+// Blocks of a split of attend_tiles: 8 against 16 took 49 against 54 us with 256
+// rows of 12001 slots and 22 against 31 us with 128 rows of 2000, but 55 against
+// 50 us with 1024 rows of 2000; 32 took 60, 49 and 65 us.
+constexpr int kMinTileBlocks = 8;
+// Rows beyond which attend_tiles takes over from attend_rows, without and with
+// weights (whose second pass after attend_rows, weigh_kernel, is the slower one
+// there): 20 rows of 8192 slots take 16 us in attend_rows and 29 us in
+// attend_tiles; 64 rows 22 and 24 us, of 16 sequences of 2000 slots 52 and 55 us;
+// 128 rows of those 58 and 71 us, but of 8192 slots and with 256 channels
+// attend_tiles is as fast or faster.  With weights 32 rows take 24 and 38 us of
+// 8192 slots, 63 and 58 us of 16 x 2000, and 64 rows 33 and 35, 97 and 80 us.
+constexpr int kManyRows = 64, kManyRowsWeighed = 32;
+// Up to this many rows z is kept for the weights: of 2, 4 and 8 rows of 32 x 2000
+// slots 29, 31 and 35 us, 69, 69 and 72 us if it is computed again.
+constexpr int kStashRows = 8;
+// attend_few, steps of 64 slots: an item has a workgroup of its own up to
+// kOwnSteps steps (at 16 steps 13 against 18 us for 4 sequences, 41 against 48 us
+// for 128), and up to one step per kItemsPerStep items (128 sequences of 2000
+// slots, 32 steps: 63 against 67 us, ragged 43 against 51; 32 sequences: 23
+// against 27 and 22 against 24 us; but 4 sequences 21 against 18 us).
+constexpr int kOwnSteps = 16, kItemsPerStep = 8;
 
 struct AttnParams {
   Cache c;
@@ -1676,7 +1694,7 @@ static bool plan(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv
   // attend_few: a set of 64 channels has to share its pair; step numbers are below 2^30
   const int64_t steps = (spanned(kFewRows) + 2 * kBlock - 1) / (2 * kBlock), cost = steps + kItemCost;
   const bool few = rows <= kFewRows && c->group >= 64 && heads * cost < (int64_t(1) << 30);
-  pl->kind = few ? Plan::FEW : rows > kManyRows ? Plan::TILES : Plan::ROWS;
+  pl->kind = few ? Plan::FEW : rows > (a->weights ? kManyRowsWeighed : kManyRows) ? Plan::TILES : Plan::ROWS;
   pl->nq = rows > kRowTile && c->head_dim < 256 ? 2 : 1;   // attend_rows
   pl->tile_rows = few ? kFewRows : pl->kind == Plan::TILES ? big_rows(c->head_dim) : pl->nq * kRowTile;
   pl->tiles = int((rows + pl->tile_rows - 1) / pl->tile_rows);
@@ -1685,11 +1703,14 @@ static bool plan(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv
   pl->nsplit = pl->chunk = 1;
   size_t part_rows;
   if (few) {
-    // one workgroup per item up to kOwnSteps steps; beyond, the grid shares all
-    // steps, at most 32 per wave (a page-table entry per lane and block)
-    if (steps > kOwnSteps) {
-      const int64_t most = few_waves(c->head_dim) * 32, need = (heads * cost + most - 1) / most;
-      pl->shared = int(need > kWantedGroups ? need : kWantedGroups);
+    // An item (sequence and head) has a workgroup of its own where it is short, or
+    // where there are items enough to even the grid out by themselves; else the
+    // grid shares all steps.  most: steps of a workgroup, 32 per wave (a
+    // page-table entry per lane and block).
+    const int64_t most = few_waves(c->head_dim) * 32;
+    if (steps > kOwnSteps && (steps > most || steps * kItemsPerStep > heads)) {
+      const int64_t need = (heads * cost + most - 1) / most;
+      pl->shared = int((need + kWantedGroups - 1) / kWantedGroups * kWantedGroups);
     }
     part_rows = size_t(pl->shared + heads) * kFewRows;
     pl->groups = pl->shared ? pl->shared : heads;

@@ -53,7 +53,11 @@ __device__ __forceinline__ uint32_t order_of(float v) {
 
 constexpr int kWaves = kSelectThreads / 64, kBins = 2048;
 constexpr int kPart = 4 * kSelectThreads;   // slots of a part, four per thread
-constexpr int kSmall = 2 * kPart;           // up to here select_kernel
+// Up to here select_kernel, of at most 16 keys a thread.  8 kv heads, keep 1024,
+// with the gather: at 16384 slots 25 us against 31 us in parts, at 12000 22
+// against 30 us (32 sequences 71 against 96 us); with 32 keys a thread 32768
+// slots take 43 us against 33 us in parts (8 sequences 65 against 58 us).
+constexpr int kSmall = 4 * kPart;
 constexpr uint32_t kZeroKey = 0x80000000u;
 // Keys below that of -inf: slots that stay anyway, and slots past the end.
 constexpr uint32_t kEnd = 1u, kPast = 0u;
@@ -148,6 +152,8 @@ __device__ __forceinline__ void weights_in_place(const EvictParams& p, const Ite
   for (int64_t i = t.m + threadIdx.x; i < p.max_len; i += kSelectThreads) wo[i] = 0.0f;
 }
 
+// PER: keys of a thread.
+template <int PER>
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParams p) {
   __shared__ SelectLds s;
   const int hk = int(blockIdx.x % unsigned(p.c.heads)), b = int(blockIdx.x / unsigned(p.c.heads));
@@ -156,10 +162,10 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
   if (t.n <= p.keep) {
     for (int i = tid; i < p.keep; i += kSelectThreads) t.kept[i] = i < t.n ? i : -1;
   } else {
-    const int each = (t.n + kWaves * 64 - 1) / (kWaves * 64), from = wave * each * 64 + lane;   // each <= 8
-    uint32_t key[kSmall / kSelectThreads];
+    const int each = (t.n + kWaves * 64 - 1) / (kWaves * 64), from = wave * each * 64 + lane;   // each <= PER
+    uint32_t key[PER];
 #pragma unroll
-    for (int e = 0; e < kSmall / kSelectThreads; e++) key[e] = e < each ? key_at(p, t, from + e * 64) : kPast;
+    for (int e = 0; e < PER; e++) key[e] = e < each ? key_at(p, t, from + e * 64) : kPast;
     // (with nothing wanted of the middle: prefix above all keys but NaN, of which 0 stay)
     uint32_t prefix = t.want > 0 ? 0u : 0xffffffffu, mask = 0;
     int rest = t.want;
@@ -167,7 +173,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
       clear_hist(s);
       int zeros = 0;
 #pragma unroll
-      for (int e = 0; e < kSmall / kSelectThreads; e++)
+      for (int e = 0; e < PER; e++)
         if (e < each) zeros += count_key(s, key[e], prefix, mask, pass);
       count_zeros(s, zeros, pass);
       __syncthreads();
@@ -178,13 +184,13 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
     }
     int above = 0, equal = 0;
 #pragma unroll
-    for (int e = 0; e < kSmall / kSelectThreads; e++) tally_key(key[e], prefix, above, equal);
+    for (int e = 0; e < PER; e++) tally_key(key[e], prefix, above, equal);
     if (lane == 0) { s.above[wave] = above; s.equal[wave] = equal; }
     __syncthreads();
     above = equal = 0;
     for (int i = 0; i < wave; i++) { above += s.above[i]; equal += s.equal[i]; }
 #pragma unroll
-    for (int e = 0; e < kSmall / kSelectThreads; e++)
+    for (int e = 0; e < PER; e++)
       if (e < each) place_key(p, t, from + e * 64, key[e], prefix, rest, above, equal);
   }
   if (p.wout != p.w) return;   // else the gather kernel moves the weights
@@ -519,7 +525,10 @@ struct LaunchEvict {
   int go() {
     const unsigned heads = unsigned(p.c.batch) * unsigned(p.c.heads);
     if (p.parts == 0) {
-      hipLaunchKernelGGL(select_kernel, dim3(heads), dim3(kSelectThreads), 0, st, p);
+      const dim3 grid(heads), threads(kSelectThreads);
+      if (p.max_len <= 4 * kSelectThreads) hipLaunchKernelGGL(select_kernel<4>, grid, threads, 0, st, p);
+      else if (p.max_len <= 8 * kSelectThreads) hipLaunchKernelGGL(select_kernel<8>, grid, threads, 0, st, p);
+      else hipLaunchKernelGGL(select_kernel<16>, grid, threads, 0, st, p);
     } else {
       const dim3 grid(unsigned(p.parts), heads), threads(kSelectThreads);
       hipLaunchKernelGGL(count_kernel, grid, threads, 0, st, p);

@@ -281,6 +281,9 @@ LONG = [
     (128, 64, 64, 1, 4, 1, [5000, 300], "float16", 2000),
     (64, 64, 32, 1, 1, 1, [70 * i % 1300 for i in range(70)], "float16", 0),          # more sequences than lanes
     (128, 64, 64, 8, 1, 1, [1100] + [1] * 130, "bfloat16", 0),                         # most at their first token
+    (64, 64, 64, 8, 2, 2, [1300, 0] + [3] * 20, "float16", 0),                         # items enough for one workgroup each
+    (256, 128, 64, 8, 4, 1, [1300, 0, 1290] + [2] * 20, "bfloat16", 0),
+    (128, 64, 32, 4, 1, 1, [9000] + [40 * i for i in range(3)], "float16", 0),
 ]
 
 
@@ -339,11 +342,12 @@ def test_no_pages(pwo):
     assert (kept == -1).all() and (n == 0).all()
 
 
-def test_eviction_of_many_slots_into_its_own_lengths(pwo):
+@pytest.mark.parametrize("lens", [[9000, 300, 8500], [17000, 300, 16500]])
+def test_eviction_of_many_slots_into_its_own_lengths(pwo, lens):
     """out_lengths may be lengths itself, also where the selection takes several launches."""
     _say("own lengths")
     torch = _torch()
-    c = Case(pwo, [9000, 300, 8500], 1, 64, 64, 128, seed=19).fill()
+    c = Case(pwo, lens, 1, 64, 64, 128, seed=19).fill()
     w = torch.rand(3, 1, c.table.shape[1] * 128, device="cuda")
     cache2 = pwo.KVCache(c.pages, 1, 64, page_tokens=128, buffer=c.cache.buffer.clone())
     w2, l2 = w.clone(), c.lengths.clone()
@@ -512,6 +516,8 @@ EVICT = [
     # more slots than one workgroup selects from
     (64, 64, 64, [8500, 0, 30, 12289], 5000, 4, 300), (64, 64, 256, [20000, 9000], 9500, 0, 0), (64, 64, 64, [9000], 40, 30, 10),
     (64, 64, 64, [8300], 10000, 1, 1),
+    (64, 64, 64, [16500, 0, 30, 24577], 5000, 4, 300), (64, 64, 64, [17000], 40, 30, 10), (64, 64, 64, [16400], 18000, 1, 1),
+    (64, 64, 64, [16384, 4096, 4097], 700, 3, 5),
 ]
 
 
@@ -543,7 +549,7 @@ def test_evict(pwo, D, g, P, lens, keep, sinks, recent, inplace):
     check_evict(c, w, keep, sinks, recent, kept, lengths, wout, read)
 
 
-@pytest.mark.parametrize("n", [400, 9000])
+@pytest.mark.parametrize("n", [400, 9000, 17000])
 def test_evict_nan_infinity_and_all_equal(pwo, n):
     _say("evict extremes", n)
     torch = _torch()
@@ -640,7 +646,7 @@ def test_captured_steps_replay(pwo):
     assert torch.equal(a[1], b[1]) and torch.equal(a[2], b[2]) and torch.equal(a[3], b[3])
 
 
-@pytest.mark.parametrize("lens,keep", [([300, 41], 90), ([9000, 100], 500)])
+@pytest.mark.parametrize("lens,keep", [([300, 41], 90), ([9000, 100], 500), ([17000, 100], 500)])
 def test_captured_chunk_and_eviction_replay(pwo, lens, keep):
     """A chunk appended, attended to with weights and evicted in place, with the lengths updated in place, captured in
     one graph: every replay equals the eager calls, bit for bit."""

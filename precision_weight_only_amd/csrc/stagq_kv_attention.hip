@@ -1058,8 +1058,10 @@ __global__ void __launch_bounds__(256) finish_kernel(const AttnParams p, unsigne
 //      makes 2.1e-4.)
 //   V  goes in as lo + s u, rounded to fp16 once; so do the probabilities.
 // The codes of the next tile are loaded while this one is computed, and unpacked
-// into the other buffer after it: one barrier per tile.  The row sums are a
-// matrix product with ones, of the probabilities as rounded.
+// into the other buffer after it: one barrier per tile.  The row sums are
+// of the probabilities before their rounding, in binary32 (a matrix product of
+// the rounded ones with 1 is 1.7 % faster, but leaves lse off by up to 1.5e-4 in
+// rows that see two slots).
 constexpr int kTileSlots = 64;
 // 16-row tiles of a wave (two hold too many registers at 256 channels), rows of a workgroup
 constexpr int big_tiles(int D) { return D == 256 ? 1 : 2; }
@@ -1212,10 +1214,7 @@ __device__ __forceinline__ void scores(const h8_t* kb, const h8_t* lb, const _Fl
 // their own rounding (two: 1.4); bf16 results are eight times as coarse.
 template <bool EXACT, int NT, int NV>
 __device__ __forceinline__ void weigh_values(const f4_t (*z)[4], const float* z_unit, const float* ref, const h8_t* vb,
-                                             int lane, f4_t* sum, f4_t (*acc)[NV]) {
-  h8_t ones;
-#pragma unroll
-  for (int e = 0; e < 8; e++) ones[e] = (_Float16)1.0f;
+                                             int lane, float* sum, f4_t (*acc)[NV]) {
 #pragma unroll
   for (int h = 0; h < 2; h++) {
     h8_t pf[NT], rest[NT];
@@ -1226,9 +1225,8 @@ __device__ __forceinline__ void weigh_values(const f4_t (*z)[4], const float* z_
         const float x = exp2_fast(fmaf(z[t][2 * h + (e >> 2)][e & 3], z_unit[t], -ref[t]));
         pf[t][e] = (_Float16)x;
         if (EXACT) rest[t][e] = (_Float16)(x - (float)pf[t][e]);
+        sum[t] += x;
       }
-      sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pf[t], sum[t], 0, 0, 0);
-      if (EXACT) sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, rest[t], sum[t], 0, 0, 0);
     }
 #pragma unroll
     for (int c = 0; c < NV; c++) {
@@ -1240,6 +1238,23 @@ __device__ __forceinline__ void weigh_values(const f4_t (*z)[4], const float* z_
       }
     }
   }
+}
+
+// fp16 rows of q scaled as bf16 ones are (exact): the second part of the sums
+// over 256 would be subnormal, and lse off by 1e-6 of its size instead of 3e-7.
+template <int NK>
+__device__ __forceinline__ float scale_half(h8_t* qf) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int ks = 0; ks < NK; ks++)
+#pragma unroll
+    for (int e = 0; e < 8; e++) amax = fmaxf(amax, fabsf((float)qf[ks][e]));
+  const float m = row_scale(max_sets(amax));
+#pragma unroll
+  for (int ks = 0; ks < NK; ks++)
+#pragma unroll
+    for (int e = 0; e < 8; e++) qf[ks][e] = (_Float16)((float)qf[ks][e] * m);
+  return 1.0f / m;
 }
 
 template <int D, int G, bool EXACT>
@@ -1269,13 +1284,15 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attend_tiles(const Attn
   h8_t qf[NT][NK], qs[NT];
   float z_unit[NT], ref[NT], top[NT];
   int from[NT], to[NT];
-  f4_t acc[NT][NV], sum[NT];
+  f4_t acc[NT][NV];
+  float sum[NT];   // of the lane's slots
 #pragma unroll
   for (int t = 0; t < NT; t++) {
     const int row = wrow + t * 16 + n;
     const bool there = row < s.rows;
     float unit;
     load_q<D>(p, b, hk, row, there, qf[t], &unit);
+    if (EXACT) unit = scale_half<NK>(qf[t]);   // fp16
     z_unit[t] = fabsf(p.scale2) * 256.0f * unit;
     if (p.scale2 < 0.0f)   // the sign goes to q, so that the largest product is the largest z
 #pragma unroll
@@ -1299,7 +1316,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attend_tiles(const Attn
     from[t] = int(f);
     to[t] = int(e);
     ref[t] = top[t] = kNone;
-    sum[t] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    sum[t] = 0.0f;
 #pragma unroll
     for (int c = 0; c < NV; c++) acc[t][c] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
@@ -1400,6 +1417,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attend_tiles(const Attn
 #pragma unroll
   for (int t = 0; t < NT; t++) {
     const int row = wrow + t * 16 + n;
+    const float l = sum_sets(sum[t]);
     if (row >= s.rows) {
       if (p.zero_rest && p.nsplit == 1 && row < p.rows)
 #pragma unroll
@@ -1407,7 +1425,6 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attend_tiles(const Attn
           *reinterpret_cast<u2_t*>(out_row(p, b, hk, row) + 16 * c + 4 * set) = u2_t{0u, 0u};
       continue;
     }
-    const float l = sum[t][0];
     if (p.nsplit == 1) {
 #pragma unroll
       for (int c = 0; c < NV; c++) put_out(p, b, hk, row, 16 * c + 4 * set, acc[t][c], l);

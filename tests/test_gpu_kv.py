@@ -342,6 +342,22 @@ def test_no_pages(pwo):
     assert (kept == -1).all() and (n == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("D,g,T,gq", [(64, 64, 40, 2), (96, 32, 9, 2), (128, 128, 29, 4), (128, 64, 1, 3), (256, 32, 20, 4)])
+@pytest.mark.parametrize("window", [1, 2])
+def test_lse_of_rows_that_see_one_or_two_slots(pwo, D, g, T, gq, window, dtype):
+    """lse holds 32 bits also where nothing averages out: z is off by 2^-22 of its terms (products of 22-bit parts, sums
+    in binary32), and e^z sums in binary32 (2^-22 with the logarithm and its scales)."""
+    _say("lse", D, g, T, gq, window, dtype)
+    torch = _torch()
+    c = Case(pwo, [200], 1, D, g, 64, dtype=dtype, seed=24).fill()
+    q = c.queries(T, gq)
+    lse = torch.zeros(q.shape[:3], device="cuda")
+    c.cache.attention(q, c.table, c.lengths, window=window, lse=lse)
+    r = kv_oracle.attention(_np(q)[0], *c.quant(0, 0), 1 / math.sqrt(D), True, window)
+    assert (np.abs(_np(lse)[0] - r["lse"]) <= 2.0 ** -22 * (2 + np.abs(r["lse"]) + r["reach_z"])).all()
+
+
 @pytest.mark.parametrize("lens", [[9000, 300, 8500], [17000, 300, 16500]])
 def test_eviction_of_many_slots_into_its_own_lengths(pwo, lens):
     """out_lengths may be lengths itself, also where the selection takes several launches."""

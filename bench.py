@@ -326,6 +326,71 @@ def read_sweep(args):
     print(json.dumps({"read_sweep": rows, "best": best, "cus": cus}), flush=True)
 
 
+def kv_sweep(args):
+    """The key/value cache in 4 bits (KVCache) at 8 kv heads x 128 channels, 32 q
+    heads, groups of 64, pages of 64 slots: attention of one token per sequence,
+    with and without accumulated weights, of a prompt, append and eviction, each
+    timed like the GEMV: one graph of calls, each on its own sequences (over 1 GB
+    of them where 64 copies hold as much), replayed behind a spin kernel.  One
+    JSON line: microseconds, the bytes and operations a call cannot do without,
+    and what rate that makes."""
+    import torch
+    import precision_weight_only_amd as pwo
+    dev = torch.device("cuda:0")
+    torch.cuda.set_device(dev)
+    H, HQ, D, G, P = 8, 32, 128, 64, 64
+    slot = H * 2 * (D // 2 + 4 * D // G)   # bytes of a token, K and V
+    rows = []
+
+    def time_call(name, B, n, T, kind, bytes_alg, flops=0):
+        pages = -(-n // P)
+        copies = max(2, min(64, (args.rot_mb << 20) // max(1, B * n * slot)))
+        if kind == "attend" and T > 8:
+            copies = 2   # bound by its products, not by what it reads
+        cache = pwo.KVCache(copies * B * pages, H, D, group=G, page_tokens=P, device=dev)
+        tables = torch.randperm(copies * B * pages, device=dev).to(torch.int32).view(copies, B, pages)
+        lengths = torch.full((B,), n, dtype=torch.int32, device=dev)
+        x = torch.randn(B, min(n, 4096), H, D, device=dev).to(torch.float16)
+        for i in range(copies):
+            for at in range(x.shape[1], n + x.shape[1], x.shape[1]):   # whole chunks, the last one up to n
+                m = min(at, n)
+                cache.append(x, x, tables[i], torch.full_like(lengths, m))
+        q = torch.randn(B, T, HQ, D, device=dev).to(torch.float16)
+        out, w = torch.empty_like(q), torch.rand(B, H, pages * P, device=dev)
+        wo, keep = torch.empty_like(w), max(1, n // 2)
+        k = x[:, :T].contiguous()
+        launch = {
+            "attend": lambda i, _: cache.attention(q, tables[i], lengths, out=out),
+            "attend_weights": lambda i, _: cache.attention(q, tables[i], lengths, out=out, weights=w),
+            "append": lambda i, _: cache.append(k, k, tables[i], lengths),
+            # to the pages of the next copy, so that every call finds the same state
+            "evict": lambda i, _: cache.evict(tables[i], lengths, w, keep=keep, sinks=4, recent=64,
+                                              out_table=tables[(i + 1) % copies], weights_out=wo),
+        }[kind]
+        launch(0, 0)
+        torch.cuda.synchronize()
+        us = graph_time(launch, copies, max(args.steps, 2 * copies), [0])
+        r = {"call": name, "sequences": B, "slots": n, "tokens": T, "us": round(us, 2), "bytes": bytes_alg,
+             "gb_s": round(bytes_alg / us / 1e3, 1)}
+        if flops:
+            r["tflop_s"] = round(flops / us / 1e6, 1)
+        rows.append(r)
+        print(f"[kv-sweep] {r}", file=sys.stderr, flush=True)
+
+    io = HQ * D * 2 * 2
+    for B, n in ((1, 256), (1, 4096), (1, 32768), (1, 131072), (16, 4096), (128, 4096)):
+        time_call("attention, one token", B, n, 1, "attend", B * (n * slot + io))
+        time_call("attention with weights, one token", B, n, 1, "attend_weights", B * (n * (slot + 8 * H) + io))
+    for B, n in ((1, 4096), (4, 4096)):
+        time_call("attention, prompt", B, n, n, "attend", B * n * (slot + io), B * HQ * 2 * n * n * D)
+    for B, T, n in ((16, 1, 4096), (128, 1, 4096), (1, 4096, 4096)):
+        time_call("append", B, n, T, "append", B * T * (slot + H * D * 2 * 2))
+    for B, n in ((1, 4096), (16, 4096), (1, 32768)):
+        # weights in and out, kept, the tokens that stay in and out
+        time_call("evict half", B, n, 1, "evict", B * n * (H * 8 + H * 4 // 2 + slot))
+    print(json.dumps({"kv_sweep": rows, "kv_heads": H, "heads": HQ, "head_dim": D, "group": G, "page_tokens": P}), flush=True)
+
+
 def sweep(args):
     """Every matrix of the attention, MLP, Phi-4 and layer-sweep workloads at each
     precision (one graph of K launches per precision, rotating image copies),
@@ -520,6 +585,8 @@ def main():
     ap.add_argument("--read-sweep", action="store_true",
                     help="time plain reads of the headline byte counts and of the LM head's over a "
                          "grid of launch shapes (threads, loads in flight, workgroups)")
+    ap.add_argument("--kv-sweep", action="store_true",
+                    help="time the key/value cache: attention, append and eviction over batches and lengths")
     ap.add_argument("--calib-copy-mb", type=int, default=0,
                     help="also run 5 device-to-device copies of this many MiB (counter calibration)")
     args = ap.parse_args()
@@ -542,6 +609,9 @@ def main():
         return
     if args.read_sweep:
         read_sweep(args)
+        return
+    if args.kv_sweep:
+        kv_sweep(args)
         return
     dev = torch.device("cuda:0")
     torch.cuda.set_device(dev)

@@ -20,7 +20,11 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNone = -1e30f;  // reference of a row that has seen nothing
 constexpr int kRowTile = 16;
 constexpr int kWantedGroups = 512;  // two workgroups per CU
-constexpr int kMinBlocks = 8;       // of a split
+// Blocks of a split of attend_rows where the grid is filled twice, and workgroups
+// up to which they may be fewer (a block per wave): 16 rows of 2000 slots take 10
+// against 11 us, 32 rows of 4 x 1000 16 against 19 us; but fewer everywhere,
+// 32 rows of 4 x 2000 28 against 20 us and 16 rows of 8000 14 against 12 us.
+constexpr int kMinBlocks = 8, kSingleGroups = 256;
 // Rules of plan(), measured with 8 kv heads of 128 channels unless said otherwise.
 // Blocks of a split of attend_tiles: 8 against 16 took 49 against 54 us with 256
 // rows of 12001 slots and 22 against 31 us with 128 rows of 2000, but 55 against
@@ -38,11 +42,12 @@ constexpr int kManyRows = 64, kManyRowsWeighed = 32;
 // slots 29, 31 and 35 us, 69, 69 and 72 us if it is computed again.
 constexpr int kStashRows = 8;
 // attend_few, steps of 64 slots: an item has a workgroup of its own up to
-// kOwnSteps steps (at 16 steps 13 against 18 us for 4 sequences, 41 against 48 us
-// for 128), and up to one step per kItemsPerStep items (128 sequences of 2000
-// slots, 32 steps: 63 against 67 us, ragged 43 against 51; 32 sequences: 23
-// against 27 and 22 against 24 us; but 4 sequences 21 against 18 us).
-constexpr int kOwnSteps = 16, kItemsPerStep = 8;
+// kOwnSteps steps (a sequence of 12 steps 10.8 us, one of 16 13.1 us and shared
+// 11.4 us, one of 24 shared 11.5 us), and up to one step per kItemsPerStep items
+// (128 sequences of 2000 slots, 32 steps: 63 against 67 us, ragged 43 against 51;
+// 32 sequences: 23 against 27 and 22 against 24 us; but 4 sequences 21 against
+// 18 us).
+constexpr int kOwnSteps = 12, kItemsPerStep = 8;
 
 struct AttnParams {
   Cache c;
@@ -595,7 +600,9 @@ __device__ __forceinline__ int prefix64(int v) {   // inclusive, over the wave
 // at number `first` and has n > 0 steps is in the workgroups first / quota ..
 // (first + n - 1) / quota, and its part in workgroup w is part w + item, which
 // no two parts share.
-constexpr int kMinQuota = 16;  // steps: four per wave
+// At least a step per wave: one sequence of 2000 slots takes 11.5 us, with 8 13.7
+// and with 16 17.4 us (of 8000 13.6, 14.7 and 19 us, of 32000 all 19 us).
+constexpr int kMinQuota = 4;
 constexpr int kItemCost = 8;
 __device__ __forceinline__ int few_cost(const AttnParams& p, int b) {
   const int n = few_steps(p, b);
@@ -1738,6 +1745,12 @@ static bool plan(const stagq_kv_cache* c, const stagq_kv_seqs* q, const stagq_kv
     const int64_t least = big ? kMinTileBlocks : kMinBlocks, unit = big ? 2 : waves;
     int64_t per = (blocks + wanted - 1) / wanted;
     per = per < least ? least : per;
+    if (!big) {   // few blocks: one workgroup per CU rather than longer splits
+      const int64_t single = base > 0 ? (kSingleGroups + base - 1) / base : 1;
+      int64_t one = (blocks + single - 1) / single;
+      one = one < waves ? waves : one;
+      per = one < per ? one : per;
+    }
     if (!big && per > 64 * waves) per = 64 * waves;   // 64 blocks per wave at most
     per = (per + unit - 1) / unit * unit;
     pl->chunk = int(per) * kBlock;
